@@ -103,7 +103,8 @@ typedef enum s2o_status {
   S2O_ERR_CUDA = 4,                /* a CUDA runtime call or launch failed */
   S2O_ERR_DEVICE_TIMEOUT = 5,      /* a bounded device wait ran out */
   S2O_ERR_NONFINITE = 6,           /* Inf/NaN in Q or K, or a non-finite score */
-  S2O_ERR_BAD_PLAN = 7             /* perm/nblocks out of range in s2o_attention */
+  S2O_ERR_BAD_PLAN = 7,            /* perm/nblocks out of range in s2o_attention */
+  S2O_ERR_BAD_CACHE = 8            /* page id, length or token range out of range (paged cache) */
 } s2o_status;
 
 enum { S2O_OUT_BF16 = 0, S2O_OUT_F32 = 1 };
@@ -357,6 +358,127 @@ s2o_status s2o_prefill_host(const s2o_config* cfg, const uint16_t* Q_host, const
                             const uint16_t* V_host, void* O_host, int32_t out_dtype,
                             int32_t* nblocks_host, void* arena, size_t arena_bytes,
                             s2o_stream_t stream);
+
+/*
+ * Serving: rotary positions, a paged key/value cache and attention over it
+ * (the pages have no counterpart; they are what a program needs around the
+ * prefill above: queries and keys are rotated before the plan, keys and
+ * values are kept in a cache, and the tokens that follow attend to it).
+ * Element types: bf16 or fp16 (S2O_TYPE_*), head dimension 128.
+ */
+enum { S2O_TYPE_BF16 = 0, S2O_TYPE_FP16 = 1 };
+enum { S2O_OUT_SAME = 0 }; /* s2o_attention_paged: O in the cache's type (or S2O_OUT_F32) */
+
+/*
+ * Rotation of a head row x at the positions p[0 .. naxes) of its token:
+ * frequency f < rot_dim / 2 turns its pair (a, b) by phi = p[axis[f]] *
+ * inv_freq[f], to (a cos phi - b sin phi, a sin phi + b cos phi).  The pair
+ * is (x[f], x[f + rot_dim/2]), or (x[2f], x[2f+1]) with `interleaved`;
+ * elements from rot_dim on pass through.  rot_dim is a multiple of 16 up to
+ * 128 (0: nothing turns), naxes 1 to 3 (time, height, width, say).  Angles are
+ * reduced in fp64, so they hold for every int32 position; sums and products
+ * are fp32, rounded once.  The struct is read by the call, not kept.
+ */
+typedef struct s2o_rotary_config {
+  int32_t rot_dim;
+  int32_t interleaved;
+  int32_t naxes;
+  int32_t reserved;
+  double inv_freq[64];
+  uint8_t axis[64];
+} s2o_rotary_config;
+
+/* Rows of 128 contiguous elements at ptr + b stride_b + t stride_t + h
+ * stride_h (strides in elements, multiples of 8; ptr 16-byte aligned). */
+typedef struct s2o_view {
+  void* ptr;
+  int64_t stride_b, stride_t, stride_h;
+} s2o_view;
+
+/*
+ * s2o_rotary -- turn the queries and keys of a prompt, from any layout into
+ * any layout: a packed token-major projection in, the head-major [B, H, N, d]
+ * of s2o_plan and s2o_attention out, say.
+ *   q, k         [B, N, Hq, 128] and [B, N, Hkv, 128] views; Hq or Hkv may be 0
+ *   positions    device int32 [naxes, B, N]
+ *   q_out, k_out views of the same extents; a view may be its own input
+ *                (in place), other overlaps are not allowed
+ *   inverse      nonzero: turn by -phi (the transposed rotation, which also
+ *                takes a gradient of the outputs to one of the inputs)
+ */
+s2o_status s2o_rotary(const s2o_rotary_config* rotary, int32_t dtype, int32_t B, int32_t N, int32_t Hq, int32_t Hkv,
+                      const s2o_view* q, const s2o_view* k, const int32_t* positions, const s2o_view* q_out,
+                      const s2o_view* k_out, int32_t inverse, s2o_stream_t stream);
+
+/*
+ * The paged cache of a batch.
+ *   k_cache, v_cache  device [num_pages, Hkv, page_size, 128], 16-byte aligned
+ *   page_table        device int32 [nseq, max_pages]: key i of sequence s is
+ *                     row i % page_size of page page_table[s, i / page_size];
+ *                     entries behind a sequence's last page are not read
+ *   q_start           device int32 [nseq + 1], q_start[0] = 0, ascending:
+ *                     sequence s brings the tokens [q_start[s], q_start[s+1]),
+ *                     at most max_q of them, none allowed; tokens from
+ *                     q_start[nseq] to Tq belong to no sequence and what the
+ *                     calls would write for them is left as it was
+ *   kv_len            device int32 [nseq]: own keys of the sequence, the new
+ *                     tokens' (its last ones) included
+ *   prefix_pages      device int32 [ceil(prefix_len / page_size)]: the pages
+ *                     of prefix_len further keys that every sequence sees
+ *                     before its own.  prefix_len is a host value: a captured
+ *                     call keeps it.  0: no prefix, prefix_pages may be NULL.
+ * The arrays on the device are read when the work runs, so a captured call
+ * follows them.  A page id outside [0, num_pages), a length above max_pages *
+ * page_size or below its new tokens, or token ranges that do not fit set the
+ * device error word (S2O_ERR_BAD_CACHE); no access leaves the buffers.
+ * Limits: page_size 16, 32, 64 or 128; Hq / Hkv at most 64.
+ */
+typedef struct s2o_cache_config {
+  int32_t Hq, Hkv, d;
+  int32_t page_size, num_pages;
+  int32_t nseq, max_pages;
+  int32_t Tq;          /* rows of the token-major tensors */
+  int32_t max_q;       /* the most new tokens of a sequence */
+  int32_t prefix_len;
+  int32_t dtype;       /* S2O_TYPE_* of queries, keys, values and caches */
+} s2o_cache_config;
+
+/*
+ * s2o_cache_append -- write the new tokens' keys (turned) and values into
+ * their pages, and turn their queries beside it.
+ *   rotary     NULL: nothing is turned
+ *   q, q_out   [Tq, Hq, 128] views (stride_b unused), both NULL: no queries;
+ *              q_out may be q
+ *   k, v       [Tq, Hkv, 128] views
+ *   positions  device int32 [naxes, Tq], or NULL: token i of a sequence's own
+ *              keys stands at prefix_len + i on every axis
+ * Two tokens whose table rows name the same page and row race for it.
+ */
+s2o_status s2o_cache_append(const s2o_cache_config* cfg, const s2o_rotary_config* rotary, const s2o_view* q,
+                            const s2o_view* k, const s2o_view* v, const int32_t* positions, const int32_t* page_table,
+                            const int32_t* q_start, const int32_t* kv_len, uint16_t* k_cache, uint16_t* v_cache,
+                            const s2o_view* q_out, s2o_stream_t stream);
+
+/*
+ * s2o_attention_paged -- exact softmax attention of the new tokens over the
+ * cache: token i of a sequence's own keys sees the whole prefix and the own
+ * keys 0 .. i.  The prefix is read once for the whole batch, each own key once.
+ *   Q    device [Tq, Hq, 128], contiguous
+ *   O    out, device [Tq, Hq, 128], in the cache's type (S2O_OUT_SAME) or fp32
+ *   lse  out, device fp32 [Tq, Hq]: log sum_j exp(s_ij); or NULL
+ *   workspace  device scratch of s2o_attention_paged_workspace_size() bytes
+ *        (on the device the call runs on), 256-byte aligned; contents need no
+ *        initialisation; calls whose work may overlap need one each
+ * Sums and accumulators are fp32; probabilities are rounded to the cache's
+ * type for the product with V.  Cached rows below the lengths must be finite;
+ * what pages hold behind them does not matter.  The result depends on the
+ * inputs and the device's SM count alone (no atomics).
+ */
+s2o_status s2o_attention_paged_workspace_size(const s2o_cache_config* cfg, size_t* bytes);
+s2o_status s2o_attention_paged(const s2o_cache_config* cfg, const uint16_t* Q, const uint16_t* k_cache,
+                               const uint16_t* v_cache, const int32_t* prefix_pages, const int32_t* page_table,
+                               const int32_t* q_start, const int32_t* kv_len, void* O, int32_t out_dtype, float* lse,
+                               void* workspace, size_t workspace_bytes, s2o_stream_t stream);
 
 /* Static description of a status code. */
 const char* s2o_status_string(s2o_status st);

@@ -22,8 +22,11 @@ OUT_BF16, OUT_F32 = 0, 1
 STATUS = {
     0: "S2O_OK", 1: "S2O_ERR_INVALID_ARG", 2: "S2O_ERR_UNSUPPORTED_SHAPE",
     3: "S2O_ERR_WORKSPACE_TOO_SMALL", 4: "S2O_ERR_CUDA", 5: "S2O_ERR_DEVICE_TIMEOUT",
-    6: "S2O_ERR_NONFINITE", 7: "S2O_ERR_BAD_PLAN",
+    6: "S2O_ERR_NONFINITE", 7: "S2O_ERR_BAD_PLAN", 8: "S2O_ERR_BAD_CACHE",
 }
+
+BF16, FP16 = 0, 1  # element types of the serving calls
+OUT_SAME = 0       # attention_paged: O in the cache's type (or OUT_F32)
 
 
 class S2OError(RuntimeError):
@@ -41,6 +44,48 @@ class Config(ctypes.Structure):
 
 def make_config(B, Hq, Hkv, N, d=128, tau=1e-3, Lq=128, Bk=64, n_sink=64, window_prev=128) -> Config:
     return Config(B, Hq, Hkv, N, d, Lq, Bk, n_sink, window_prev, float(tau))
+
+
+class RotaryConfig(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("naxes", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("inv_freq", ctypes.c_double * 64), ("axis", ctypes.c_uint8 * 64)]
+
+
+class View(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_t", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64)]
+
+
+class CacheConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("Hq", "Hkv", "d", "page_size", "num_pages", "nseq", "max_pages", "Tq",
+                                              "max_q", "prefix_len", "dtype")]
+
+
+def make_rotary(rot_dim: int = 128, theta: float = 10000.0, sections=None, interleaved: bool = False,
+                inv_freq=None) -> RotaryConfig:
+    """Rotation of the first rot_dim elements of a head.  sections: how many of
+    the rot_dim/2 frequencies, in order, go by each position axis (None: one
+    axis); inv_freq: the frequencies themselves, in place of
+    theta^(-2 i / rot_dim)."""
+    if rot_dim < 0 or rot_dim > 128 or rot_dim % 2:
+        raise S2OError(2, "make_rotary: rot_dim")
+    F = rot_dim // 2
+    sections = (F,) if sections is None else tuple(int(n) for n in sections)
+    if not 1 <= len(sections) <= 3 or any(n < 0 for n in sections) or sum(sections) != F:
+        raise S2OError(1, "make_rotary: sections must be 1 to 3 counts that add up to rot_dim / 2")
+    freq = [theta ** (-2.0 * i / rot_dim) for i in range(F)] if inv_freq is None else [float(x) for x in inv_freq]
+    if len(freq) != F:
+        raise S2OError(1, "make_rotary: inv_freq needs rot_dim / 2 values")
+    r = RotaryConfig(rot_dim, int(interleaved), len(sections), 0)
+    r.inv_freq[:F] = freq
+    r.axis[:F] = [a for a, n in enumerate(sections) for _ in range(n)]
+    return r
+
+
+def make_cache(Hq, Hkv, page_size, num_pages, nseq, max_pages, Tq, max_q=1, prefix_len=0, dtype=BF16,
+               d=128) -> CacheConfig:
+    """The paged cache of a batch, as include/s2o.h describes it."""
+    return CacheConfig(Hq, Hkv, d, page_size, num_pages, nseq, max_pages, Tq, max_q, prefix_len, dtype)
 
 
 _lib = None
@@ -85,6 +130,14 @@ def lib() -> ctypes.CDLL:
         L.s2o_last_stage_times.argtypes = [ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_char_p),
                                            ctypes.c_int32]
         L.s2o_last_stage_times.restype = ctypes.c_int32
+        _R, _V, _C = ctypes.POINTER(RotaryConfig), ctypes.POINTER(View), ctypes.POINTER(CacheConfig)
+        i32 = ctypes.c_int32
+        L.s2o_rotary.argtypes = [_R, i32, i32, i32, i32, i32, _V, _V, _P, _V, _V, i32, _P]
+        L.s2o_cache_append.argtypes = [_C, _R, _V, _V, _V, _P, _P, _P, _P, _P, _P, _V, _P]
+        L.s2o_attention_paged_workspace_size.argtypes = [_C, ctypes.POINTER(ctypes.c_size_t)]
+        L.s2o_attention_paged.argtypes = [_C, _P, _P, _P, _P, _P, _P, _P, _P, i32, _P, _P, ctypes.c_size_t, _P]
+        for name in ("s2o_rotary", "s2o_cache_append", "s2o_attention_paged_workspace_size", "s2o_attention_paged"):
+            getattr(L, name).restype = ctypes.c_int
         for name in ("s2o_plan_workspace_size", "s2o_plan", "s2o_plan_filtered", "s2o_plan_noalloc", "s2o_plan_contiguous", "s2o_attention", "s2o_attention_bounded", "s2o_attention_online",
                      "s2o_block_truth_workspace_size", "s2o_block_truth", "s2o_plan_qperm_workspace_size",
                      "s2o_plan_qperm", "s2o_attention_qperm",
@@ -275,6 +328,190 @@ def prefill_host(cfg: Config, Q_host, K_host, V_host, O_host, arena, nblocks_hos
                                   out_dtype, _ptr(nblocks_host), _ptr(arena), arena.numel(), _stream(stream)),
            "s2o_prefill_host")
     return O_host
+
+
+# --- serving: rotary positions, the paged cache and attention over it -----------
+# These calls check what only the tensors know (type, shape, layout, device);
+# sizes and pointers are checked by the library.
+
+
+def _torch_type(dtype: int):
+    import torch
+    return torch.float16 if dtype == FP16 else torch.bfloat16
+
+
+def _refuse(what: str):
+    raise S2OError(1, what)
+
+
+def _view3(t, what, H, T, dtype, device):
+    """[T, H, 128] with contiguous rows."""
+    if t.dtype != dtype or t.device != device or t.shape != (T, H, 128) or (t.stride(2) != 1 and t.numel()):
+        _refuse(f"{what}: want a {dtype} [{T}, {H}, 128] tensor with contiguous rows on {device}, "
+                f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+    return View(t.data_ptr(), 0, t.stride(0), t.stride(1))
+
+
+def _view4(t, what, B, N, H, dtype, device):
+    """[B, N, H, 128] with contiguous rows."""
+    if t.dtype != dtype or t.device != device or t.shape != (B, N, H, 128) or (t.stride(3) != 1 and t.numel()):
+        _refuse(f"{what}: want a {dtype} [{B}, {N}, {H}, 128] tensor with contiguous rows on {device}, "
+                f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+    return View(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+
+
+def _plain(t, what, shape, dtype, device):
+    """A contiguous tensor of this shape."""
+    if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
+        _refuse(f"{what}: want a contiguous {dtype} tensor of {tuple(shape)} on {device}, "
+                f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+    return t.data_ptr()
+
+
+def _empty(shape, dtype, device, stream):
+    """Memory that belongs to the stream it is used on."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _call_on(device, stream, fn, name, *args):
+    """fn(*args, stream) with the tensors' device current."""
+    import torch
+    if device.type != "cuda":
+        _refuse(f"{name}: the tensors are on {device}, not on a CUDA device")
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, (stream or torch.cuda.current_stream(device)).cuda_stream), name)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, (stream or torch.cuda.current_stream(device)).cuda_stream), name)
+
+
+def rotary(r: RotaryConfig, q, k, positions, q_out=None, k_out=None, inverse: bool = False, stream=None):
+    """s2o_rotary: q [B, N, Hq, 128] and k [B, N, Hkv, 128] (any strides; either
+    may be None) turned at positions int32 [naxes, B, N]; returns (q_out, k_out)
+    of the same shapes.  Outputs that are not given are allocated head-major
+    (q_out.transpose(1, 2) is contiguous: what plan and attention read), or
+    token-major for the inverse, which takes head-major gradients back."""
+    import torch
+    x = q if q is not None else k
+    if x is None or x.dim() != 4:
+        _refuse("rotary: q or k must be a [B, N, H, 128] tensor")
+    B, N, dev, t = x.shape[0], x.shape[1], x.device, x.dtype
+    if t is not torch.bfloat16 and t is not torch.float16:
+        _refuse(f"rotary: {t} is neither bfloat16 nor float16")
+    sides = []
+    for name, src, dst in (("q", q, q_out), ("k", k, k_out)):
+        if src is None:
+            sides.append((0, None, None, None))
+            continue
+        if src.dim() != 4:
+            _refuse(f"rotary: {name} must be a [B, N, H, 128] tensor")
+        H = src.shape[2]
+        vin = _view4(src, "rotary: " + name, B, N, H, t, dev)
+        if dst is None:
+            dst = (_empty((B, N, H, 128), t, dev, stream) if inverse else
+                   _empty((B, H, N, 128), t, dev, stream).transpose(1, 2))
+        sides.append((H, vin, _view4(dst, f"rotary: {name}_out", B, N, H, t, dev), dst))
+    pos = _plain(positions, "rotary: positions", (r.naxes, B, N), torch.int32, dev)
+    (Hq, qi, qo, qd), (Hkv, ki, ko, kd) = sides
+    _call_on(dev, stream, lib().s2o_rotary, "s2o_rotary", r, FP16 if t is torch.float16 else BF16, B, N, Hq, Hkv, qi,
+             ki, pos, qo, ko, int(inverse))
+    return qd, kd
+
+
+def alloc_cache(cfg: CacheConfig, device="cuda"):
+    """(k_cache, v_cache) of the config, zeroed."""
+    import torch
+    shape = (cfg.num_pages, cfg.Hkv, cfg.page_size, cfg.d)
+    return tuple(torch.zeros(shape, dtype=_torch_type(cfg.dtype), device=device) for _ in range(2))
+
+
+def _cache_args(cfg, k_cache, v_cache, page_table, q_start, kv_len, dev, t):
+    import torch
+    shape = (cfg.num_pages, cfg.Hkv, cfg.page_size, cfg.d)
+    return (_plain(k_cache, "k_cache", shape, t, dev), _plain(v_cache, "v_cache", shape, t, dev),
+            _plain(page_table, "page_table", (cfg.nseq, cfg.max_pages), torch.int32, dev),
+            _plain(q_start, "q_start", (cfg.nseq + 1,), torch.int32, dev),
+            _plain(kv_len, "kv_len", (cfg.nseq,), torch.int32, dev))
+
+
+def cache_append(cfg: CacheConfig, q, k, v, k_cache, v_cache, page_table, q_start, kv_len, rotary=None,
+                 positions=None, q_out=None, stream=None):
+    """s2o_cache_append: k and v [Tq, Hkv, 128] (any strides) into the caches, k
+    turned by `rotary` (None: as it is); q [Tq, Hq, 128] (or None) turned into
+    q_out (allocated when not given).  positions int32 [naxes, Tq], or None:
+    prefix_len + the token's place in its sequence.  Returns q_out."""
+    import torch
+    dev, t, T = k.device, _torch_type(cfg.dtype), cfg.Tq
+    qv = qo = None
+    if q is not None:
+        qv = _view3(q, "cache_append: q", cfg.Hq, T, t, dev)
+        if q_out is None:
+            q_out = _empty((T, cfg.Hq, 128), t, dev, stream)
+        qo = _view3(q_out, "cache_append: q_out", cfg.Hq, T, t, dev)
+    elif q_out is not None:
+        _refuse("cache_append: q_out without q")
+    kv = _view3(k, "cache_append: k", cfg.Hkv, T, t, dev)
+    vv = _view3(v, "cache_append: v", cfg.Hkv, T, t, dev)
+    kc, vc, table, qs, kl = _cache_args(cfg, k_cache, v_cache, page_table, q_start, kv_len, dev, t)
+    pos = None
+    if positions is not None:
+        if rotary is None:
+            _refuse("cache_append: positions without a rotation")
+        pos = _plain(positions, "cache_append: positions", (rotary.naxes, T), torch.int32, dev)
+    _call_on(dev, stream, lib().s2o_cache_append, "s2o_cache_append", cfg, rotary, qv, kv, vv, pos, table, qs, kl, kc,
+             vc, qo)
+    return q_out
+
+
+def attention_paged_workspace_size(cfg: CacheConfig) -> int:
+    """Bytes for the current device."""
+    n = ctypes.c_size_t(0)
+    _check(lib().s2o_attention_paged_workspace_size(cfg, n), "s2o_attention_paged_workspace_size")
+    return n.value
+
+
+def alloc_attention_paged(cfg: CacheConfig, device="cuda"):
+    """A workspace for attention_paged calls of this config on `device` (one per
+    stream or captured graph whose work may overlap another's)."""
+    import torch
+    with torch.cuda.device(device):
+        return torch.empty(attention_paged_workspace_size(cfg), dtype=torch.uint8, device=device)
+
+
+def attention_paged(cfg: CacheConfig, q, k_cache, v_cache, page_table, q_start, kv_len, prefix_pages=None, O=None,
+                    lse=None, workspace=None, out_dtype: int = OUT_SAME, stream=None):
+    """s2o_attention_paged: q [Tq, Hq, 128] over the caches; returns (O, lse).
+    O, lse (float32 [Tq, Hq]) and the workspace are allocated when not given;
+    rows behind q_start[nseq] are left as they were."""
+    import torch
+    dev, t, T = q.device, _torch_type(cfg.dtype), cfg.Tq
+    qp = _plain(q, "attention_paged: q", (T, cfg.Hq, 128), t, dev)
+    kc, vc, table, qs, kl = _cache_args(cfg, k_cache, v_cache, page_table, q_start, kv_len, dev, t)
+    pre = None
+    if cfg.prefix_len > 0:
+        if prefix_pages is None:
+            _refuse("attention_paged: prefix_len without prefix_pages")
+        pre = _plain(prefix_pages, "attention_paged: prefix_pages", (-(-cfg.prefix_len // max(1, cfg.page_size)),),
+                     torch.int32, dev)
+    to = torch.float32 if out_dtype == OUT_F32 else t
+    if O is None:
+        O = _empty((T, cfg.Hq, 128), to, dev, stream)
+    if lse is None:
+        lse = _empty((T, cfg.Hq), torch.float32, dev, stream)
+    if workspace is None:
+        with torch.cuda.device(dev):
+            workspace = _empty((attention_paged_workspace_size(cfg),), torch.uint8, dev, stream)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        _refuse("attention_paged: workspace")
+    _call_on(dev, stream, lib().s2o_attention_paged, "s2o_attention_paged", cfg, qp, kc, vc, pre, table, qs, kl,
+             _plain(O, "attention_paged: O", (T, cfg.Hq, 128), to, dev), out_dtype,
+             _plain(lse, "attention_paged: lse", (T, cfg.Hq), torch.float32, dev), workspace.data_ptr(),
+             workspace.numel() * workspace.element_size())
+    return O, lse
 
 
 def last_device_error(stream=None) -> int:

@@ -1,0 +1,258 @@
+// C ABI of the rotation, the paged-cache append and the paged attention:
+// argument checks, workspace layout and launches.  Included by s2o_api.cu,
+// whose helpers (alignment, tensor-map encoder, launch count) it uses.
+#pragma once
+
+namespace {
+
+constexpr double kTwoPi = 6.283185307179586476925286766559;
+
+s2o_status rotary_table(const s2o_rotary_config* r, bool inverse, RotaryTable* t) {
+  std::memset(t, 0, sizeof(*t));
+  t->sign = inverse ? -1.f : 1.f;
+  if (!r) return S2O_OK;  // no rotation
+  if (r->rot_dim < 0 || r->naxes < 1 || r->naxes > 3) return S2O_ERR_INVALID_ARG;
+  if (r->rot_dim % 16 || r->rot_dim > kD) return S2O_ERR_UNSUPPORTED_SHAPE;
+  t->rot = r->rot_dim;
+  t->adjacent = r->interleaved != 0;
+  t->naxes = r->naxes;
+  for (int i = 0; i < r->rot_dim / 2; ++i) {
+    if (!std::isfinite(r->inv_freq[i]) || r->axis[i] >= r->naxes) return S2O_ERR_INVALID_ARG;
+    t->turns[i] = r->inv_freq[i] / kTwoPi;
+    t->axis[i] = r->axis[i];
+  }
+  return S2O_OK;
+}
+
+bool take_view(const s2o_view* v, RowView* out) {
+  if (!v->ptr || !aligned16(v->ptr)) return false;
+  if (v->stride_b % 8 || v->stride_t % 8 || v->stride_h % 8) return false;  // rows stay 16-byte aligned
+  out->p = static_cast<uint16_t*>(v->ptr);
+  out->sb = v->stride_b;
+  out->st = v->stride_t;
+  out->sh = v->stride_h;
+  return true;
+}
+
+s2o_status check_cache(const s2o_cache_config* c) {
+  if (!c) return S2O_ERR_INVALID_ARG;
+  if (c->Hq <= 0 || c->Hkv <= 0 || c->d <= 0 || c->page_size <= 0 || c->num_pages <= 0 || c->nseq <= 0 ||
+      c->max_pages <= 0 || c->Tq < 0 || c->max_q <= 0 || c->prefix_len < 0 || c->Hq % c->Hkv)
+    return S2O_ERR_INVALID_ARG;
+  if (c->dtype != S2O_TYPE_BF16 && c->dtype != S2O_TYPE_FP16) return S2O_ERR_INVALID_ARG;
+  if (c->d != kD) return S2O_ERR_UNSUPPORTED_SHAPE;
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+    return S2O_ERR_UNSUPPORTED_SHAPE;
+  // row numbers of the caches are 32-bit coordinates, key numbers 32-bit
+  if ((int64_t)c->num_pages * c->Hkv * c->page_size >= (int64_t)INT32_MAX ||
+      (int64_t)c->max_pages * c->page_size + c->prefix_len >= (int64_t)INT32_MAX - 512)
+    return S2O_ERR_UNSUPPORTED_SHAPE;
+  if (c->Hq / c->Hkv > 64 || (int64_t)c->Tq * c->Hq >= (int64_t)INT32_MAX) return S2O_ERR_UNSUPPORTED_SHAPE;
+  return S2O_OK;
+}
+
+int log2_of(int x) {
+  int l = 0;
+  while ((1 << l) < x) ++l;
+  return l;
+}
+
+int sm_count() {
+  int dev = 0, n = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n;
+}
+
+// The paged attention's plan of kernels for a call: a rule on sizes the host
+// knows, so the workspace size and the launches agree.
+struct PagedPlan {
+  int R;              // row tiles of 16 of the decode kernel
+  PagedCut cut;
+};
+PagedPlan paged_plan(const s2o_cache_config* c) {
+  PagedPlan p;
+  const int G = c->Hq / c->Hkv;
+  const int64_t rows = std::max((int64_t)std::min(c->max_q, c->Tq), (int64_t)(c->prefix_len > 0 ? c->Tq : 0)) * G;
+  p.R = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
+  if (16 * p.R < G) p.R = G <= 32 ? 2 : 4;
+  p.cut.tpt = 16 * p.R / G;
+  p.cut.kt_log2 = 6;
+  p.cut.prefix_items = c->prefix_len > 0;
+  p.cut.own_items = 1;
+  p.cut.walk_prefix = 0;
+  return p;
+}
+
+struct PagedWs {
+  int64_t* units;
+  int2* meta;
+  PagedPart part;
+  size_t bytes;
+};
+PagedWs paged_layout(const s2o_cache_config* c, const PagedPlan& p, int n, void* base) {
+  PagedWs w{};
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* q = static_cast<uint8_t*>(base) + off;
+    off += round256(bytes);
+    return static_cast<void*>(q);
+  };
+  const size_t rows = (size_t)c->Tq * c->Hq;
+  w.units = static_cast<int64_t*>(take(256));
+  w.meta = static_cast<int2*>(take((size_t)c->Tq * c->Hkv * sizeof(int2)));
+  for (int k = 0; k < 2; ++k) {
+    if (c->prefix_len == 0) continue;  // whole items are the result
+    w.part.dense[k] = static_cast<float*>(take(rows * kD * sizeof(float)));
+    w.part.dense_ml[k] = static_cast<float2*>(take(rows * sizeof(float2)));
+  }
+  w.part.rows = 16 * p.R;
+  w.part.slots = static_cast<float*>(take((size_t)2 * n * w.part.rows * kD * sizeof(float)));
+  w.part.slots_ml = static_cast<float2*>(take((size_t)2 * n * w.part.rows * sizeof(float2)));
+  w.bytes = off;
+  return w;
+}
+
+template <bool FP16, int R>
+cudaError_t launch_decode(const PagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, int n, cudaStream_t s) {
+  // the attribute belongs to the function on the current device; setting it
+  // again costs less than a microsecond
+  cudaError_t e = cudaFuncSetAttribute(k_paged_decode<FP16, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)PgDecode<R>::kSmem);
+  if (e != cudaSuccess) return e;
+  k_paged_decode<FP16, R><<<n, PgDecode<R>::kThreads, PgDecode<R>::kSmem, s>>>(a, k, v);
+  return cudaGetLastError();
+}
+template <bool FP16>
+cudaError_t launch_decode_r(int R, const PagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, int n,
+                            cudaStream_t s) {
+  return R == 1 ? launch_decode<FP16, 1>(a, k, v, n, s)
+                : (R == 2 ? launch_decode<FP16, 2>(a, k, v, n, s) : launch_decode<FP16, 4>(a, k, v, n, s));
+}
+
+}  // namespace
+
+extern "C" {
+
+s2o_status s2o_rotary(const s2o_rotary_config* rotary, int32_t dtype, int32_t B, int32_t N, int32_t Hq, int32_t Hkv,
+                      const s2o_view* q, const s2o_view* k, const int32_t* positions, const s2o_view* q_out,
+                      const s2o_view* k_out, int32_t inverse, s2o_stream_t stream) {
+  t_launches = 0;
+  if (!rotary || B < 0 || N < 0 || Hq < 0 || Hkv < 0 || (dtype != S2O_TYPE_BF16 && dtype != S2O_TYPE_FP16))
+    return S2O_ERR_INVALID_ARG;
+  RotaryArgs a;
+  s2o_status st = rotary_table(rotary, inverse != 0, &a.r);
+  if (st != S2O_OK) return st;
+  if (B == 0 || N == 0 || Hq + (int64_t)Hkv == 0) return S2O_OK;
+  if ((int64_t)Hq + Hkv > 4096) return S2O_ERR_UNSUPPORTED_SHAPE;
+  if (!positions || (Hq && (!q || !q_out)) || (Hkv && (!k || !k_out))) return S2O_ERR_INVALID_ARG;
+  std::memset(&a.q, 0, 4 * sizeof(RowView));
+  if (Hq && (!take_view(q, &a.q) || !take_view(q_out, &a.qo))) return S2O_ERR_INVALID_ARG;
+  if (Hkv && (!take_view(k, &a.k) || !take_view(k_out, &a.ko))) return S2O_ERR_INVALID_ARG;
+  a.pos = positions;
+  a.B = B; a.N = N; a.Hq = Hq; a.Hkv = Hkv;
+  const int64_t total = (int64_t)B * N;
+  a.tb = kRotMaxTokens;
+  while (a.tb > 1 && total < (int64_t)a.tb * 148 * 4) a.tb >>= 1;
+  const int64_t blocks = (total + a.tb - 1) / a.tb;
+  if (blocks > INT32_MAX) return S2O_ERR_UNSUPPORTED_SHAPE;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (dtype == S2O_TYPE_FP16) k_rotary<true><<<(unsigned)blocks, kRotThreads, 0, s>>>(a);
+  else k_rotary<false><<<(unsigned)blocks, kRotThreads, 0, s>>>(a);
+  ++t_launches;
+  return launch_status();
+}
+
+s2o_status s2o_cache_append(const s2o_cache_config* cfg, const s2o_rotary_config* rotary, const s2o_view* q,
+                            const s2o_view* k, const s2o_view* v, const int32_t* positions, const int32_t* page_table,
+                            const int32_t* q_start, const int32_t* kv_len, uint16_t* k_cache, uint16_t* v_cache,
+                            const s2o_view* q_out, s2o_stream_t stream) {
+  t_launches = 0;
+  s2o_status st = check_cache(cfg);
+  if (st != S2O_OK) return st;
+  AppendArgs a;
+  st = rotary_table(rotary, false, &a.r);
+  if (st != S2O_OK) return st;
+  if (!k || !v || !page_table || !q_start || !kv_len || !k_cache || !v_cache || !q != !q_out)
+    return S2O_ERR_INVALID_ARG;
+  if (!aligned16(k_cache) || !aligned16(v_cache)) return S2O_ERR_INVALID_ARG;
+  std::memset(&a.q, 0, 4 * sizeof(RowView));
+  if (cfg->Tq == 0) return S2O_OK;
+  if (!take_view(k, &a.k) || !take_view(v, &a.v)) return S2O_ERR_INVALID_ARG;
+  if (q && (!take_view(q, &a.q) || !take_view(q_out, &a.qo))) return S2O_ERR_INVALID_ARG;
+  if ((int64_t)cfg->Hq + 2 * (int64_t)cfg->Hkv > 4096) return S2O_ERR_UNSUPPORTED_SHAPE;
+  a.pos = positions;
+  a.table = page_table; a.q_start = q_start; a.kv_len = kv_len;
+  a.kc = k_cache; a.vc = v_cache;
+  a.Hq = cfg->Hq; a.Hkv = cfg->Hkv; a.page_log2 = log2_of(cfg->page_size); a.num_pages = cfg->num_pages;
+  a.nseq = cfg->nseq; a.max_pages = cfg->max_pages; a.Tq = cfg->Tq; a.max_q = cfg->max_q; a.prefix = cfg->prefix_len;
+  a.tb = kRotMaxTokens;
+  while (a.tb > 1 && cfg->Tq < a.tb * 148 * 4) a.tb >>= 1;
+  const unsigned blocks = ((unsigned)cfg->Tq + a.tb - 1) / a.tb;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (cfg->dtype == S2O_TYPE_FP16) k_cache_append<true><<<blocks, kRotThreads, 0, s>>>(a);
+  else k_cache_append<false><<<blocks, kRotThreads, 0, s>>>(a);
+  ++t_launches;
+  return launch_status();
+}
+
+s2o_status s2o_attention_paged_workspace_size(const s2o_cache_config* cfg, size_t* bytes) {
+  s2o_status st = check_cache(cfg);
+  if (st != S2O_OK) return st;
+  if (!bytes) return S2O_ERR_INVALID_ARG;
+  *bytes = paged_layout(cfg, paged_plan(cfg), sm_count(), nullptr).bytes;
+  return S2O_OK;
+}
+
+s2o_status s2o_attention_paged(const s2o_cache_config* cfg, const uint16_t* Q, const uint16_t* k_cache,
+                               const uint16_t* v_cache, const int32_t* prefix_pages, const int32_t* page_table,
+                               const int32_t* q_start, const int32_t* kv_len, void* O, int32_t out_dtype, float* lse,
+                               void* workspace, size_t workspace_bytes, s2o_stream_t stream) {
+  t_launches = 0;
+  s2o_status st = check_cache(cfg);
+  if (st != S2O_OK) return st;
+  if (!Q || !k_cache || !v_cache || !page_table || !q_start || !kv_len || !O || !workspace ||
+      (cfg->prefix_len > 0 && !prefix_pages))
+    return S2O_ERR_INVALID_ARG;
+  if (out_dtype != S2O_OUT_SAME && out_dtype != S2O_OUT_F32) return S2O_ERR_INVALID_ARG;
+  if (!aligned16(Q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(O) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return S2O_ERR_INVALID_ARG;
+  const int n = sm_count();
+  const PagedPlan p = paged_plan(cfg);
+  const PagedWs w = paged_layout(cfg, p, n, workspace);
+  if (workspace_bytes < w.bytes) return S2O_ERR_WORKSPACE_TOO_SMALL;
+  if (cfg->Tq == 0) return S2O_OK;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  PagedArgs a{};
+  PagedGeom& g = a.g;
+  g.table = page_table; g.prefix_pages = prefix_pages; g.q_start = q_start; g.kv_len = kv_len;
+  g.Hq = cfg->Hq; g.Hkv = cfg->Hkv; g.G = cfg->Hq / cfg->Hkv; g.nseq = cfg->nseq; g.max_pages = cfg->max_pages;
+  g.num_pages = cfg->num_pages; g.page_log2 = log2_of(cfg->page_size); g.Tq = cfg->Tq; g.max_q = cfg->max_q;
+  g.prefix = cfg->prefix_len;
+  a.c = p.cut;
+  a.Q = Q; a.O = O; a.lse = lse; a.part = w.part; a.meta = w.meta; a.units = w.units;
+  a.out_f32 = out_dtype == S2O_OUT_F32;
+  a.direct = cfg->prefix_len == 0;
+  CUtensorMap tmK, tmV;
+  const uint64_t rows = (uint64_t)cfg->num_pages * cfg->Hkv * cfg->page_size;
+  const uint32_t box = (uint32_t)std::min(cfg->page_size, 64);
+  if (!encode_rows_map(&tmK, k_cache, rows, box) || !encode_rows_map(&tmV, v_cache, rows, box)) return S2O_ERR_CUDA;
+  const bool fp16 = cfg->dtype == S2O_TYPE_FP16;
+  if ((fp16 ? launch_decode_r<true>(p.R, a, tmK, tmV, n, s) : launch_decode_r<false>(p.R, a, tmK, tmV, n, s)) !=
+      cudaSuccess)
+    return S2O_ERR_CUDA;
+  ++t_launches;
+  JoinArgs j{};
+  j.g = g;
+  j.prefix.part = w.part; j.prefix.c = p.cut; j.prefix.units = w.units; j.prefix.n = n; j.prefix.on = cfg->prefix_len > 0;
+  j.own = j.prefix;
+  j.own.on = 1;
+  j.meta = w.meta; j.O = O; j.lse = lse; j.out_f32 = a.out_f32;
+  const unsigned blocks = (unsigned)(((int64_t)cfg->Tq * cfg->Hq + 7) / 8);
+  if (fp16) k_paged_join<true><<<blocks, 256, 0, s>>>(j);
+  else k_paged_join<false><<<blocks, 256, 0, s>>>(j);
+  ++t_launches;
+  return launch_status();
+}
+
+}  // extern "C"

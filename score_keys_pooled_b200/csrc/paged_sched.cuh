@@ -1,0 +1,318 @@
+// How the paged attention's work is cut: items, units and the share of a CTA.
+//
+// An item is a tile of query rows of one KV head against one list of keys.
+// Rows of a tile are ordered token-major: row r is token tok0 + r / G, query
+// head kvh * G + r % G.  There are two lists of items:
+//   prefix items   every token of the batch, tile after tile, against the
+//                  shared prefix (the prefix is read once for all rows of a
+//                  tile, whichever sequences they belong to);
+//   own items      the new tokens of one sequence, tile after tile, against
+//                  the sequence's own keys, causal; with `walk_prefix` the
+//                  prefix keys come first in the same item (long chunks fill
+//                  a tile by themselves, so nothing has to be joined later).
+// A unit is one tile of kt keys of an item.  The U units, in the order prefix
+// items (kvh, row tile), own items (sequence, kvh, row tile), are cut evenly:
+// CTA c of n takes units [c U / n, (c + 1) U / n), so the split follows the
+// actual lengths, which only the device knows, and every CTA reads the same
+// number of key tiles.  A CTA's part of an item is a piece; a piece that is
+// not a whole item leaves its rows' (reference, sum, accumulator) in slot
+// 2c (the item began in an earlier CTA) or 2c + 1 (it began here and goes
+// on), at most one of each per CTA.
+#pragma once
+
+#include "rotary.cuh"
+
+namespace s2o {
+
+struct PagedGeom {
+  const int32_t* table;         // [nseq, max_pages]
+  const int32_t* prefix_pages;  // [ceil(prefix / page)]
+  const int32_t* q_start;       // [nseq + 1]
+  const int32_t* kv_len;        // [nseq]
+  int Hq, Hkv, G, nseq, max_pages, num_pages, page_log2, Tq, max_q, prefix;
+};
+
+// What one kernel makes of it.
+struct PagedCut {
+  int tpt;          // tokens of a row tile
+  int kt_log2;      // keys of a unit
+  int prefix_items; // prefix items exist
+  int own_items;    // own items exist
+  int walk_prefix;  // own items start with the prefix's tiles
+};
+
+struct SeqInfo {
+  int q0, qlen, len;  // first token, tokens, own keys (the tokens' included)
+};
+
+// A sequence's numbers, checked; qlen 0 where it has no tokens or they are
+// out of range (then the error word is set).
+__device__ __forceinline__ SeqInfo seq_info(const PagedGeom& g, int s) {
+  SeqInfo i;
+  i.q0 = g.q_start[s];
+  const int q1 = g.q_start[s + 1];
+  i.len = g.kv_len[s];
+  const int64_t n = (int64_t)q1 - i.q0;
+  i.qlen = (int)n;
+  if (n == 0 && (s > 0 || i.q0 == 0)) return i;
+  if (i.q0 < 0 || (s == 0 && i.q0 != 0) || n < 0 || q1 > g.Tq || n > g.max_q || i.len < n ||
+      i.len > ((int64_t)g.max_pages << g.page_log2)) {
+    set_error(kErrBadCache);
+    i.qlen = 0;
+  }
+  return i;
+}
+
+// tokens of the batch: rows behind the last sequence belong to nobody
+__device__ __forceinline__ int batch_tokens(const PagedGeom& g) { return max(0, min(g.q_start[g.nseq], g.Tq)); }
+
+// sum over i < n of floor((a i + b) / m), n, a, b >= 0, m > 0
+__host__ __device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+  int64_t r = 0;
+  while (n > 0) {
+    if (a >= m) { r += n * (n - 1) / 2 * (a / m); a %= m; }
+    if (b >= m) { r += n * (b / m); b %= m; }
+    const int64_t y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const int64_t t = m; m = a; a = t;
+  }
+  return r;
+}
+
+struct OwnUnits {
+  int nrt;       // row tiles
+  int np;        // prefix tiles of each (walk_prefix)
+  int len, off;  // own keys; own keys before the first new token
+  int tpt, kt_log2;
+  // units of the first rt row tiles: tile i < nrt - 1 sees off + (i + 1) tpt keys, the last one all
+  __host__ __device__ int64_t before(int rt) const {
+    if (rt <= 0) return 0;
+    const int64_t kt = (int64_t)1 << kt_log2;
+    int64_t u = (int64_t)rt * np + floor_sum(rt < nrt ? rt : rt - 1, kt, tpt, (int64_t)off + tpt + kt - 1);
+    if (rt >= nrt) u += (len + kt - 1) >> kt_log2;
+    return u;
+  }
+};
+
+__host__ __device__ __forceinline__ OwnUnits own_units(int qlen, int len, int prefix, const PagedCut& c) {
+  OwnUnits u;
+  u.nrt = (qlen + c.tpt - 1) / c.tpt;
+  u.np = c.walk_prefix ? (int)(((int64_t)prefix + (1 << c.kt_log2) - 1) >> c.kt_log2) : 0;
+  u.len = len;
+  u.off = len - qlen;
+  u.tpt = c.tpt;
+  u.kt_log2 = c.kt_log2;
+  return u;
+}
+
+__host__ __device__ __forceinline__ int64_t share_begin(int64_t U, int n, int c) { return U * c / n; }
+// the CTA whose share holds unit u
+__host__ __device__ __forceinline__ int share_owner(int64_t U, int n, int64_t u) {
+  return (int)(((u + 1) * n - 1) / U);
+}
+
+// A piece: the CTA's part of an item.
+struct Piece {
+  int kind;          // 0 prefix item, 1 own item, -1 no more
+  int seq, kvh;
+  int tok0, ntok;    // tokens of the row tile
+  int off;           // own: key index of token tok0 (it sees own keys 0 .. off)
+  int len;           // keys of the list the rows of the tile can reach (prefix: all of it)
+  int np;            // leading tiles that are the prefix's
+  int tile0, tile1;  // tiles of the item the piece covers
+  int c0, c1;        // CTAs that hold the item's first and last unit
+  int first;         // the piece begins the item
+};
+
+// Walks the pieces of a CTA's share.  All threads of a block call
+// `sched_begin` once; the state is then advanced by whoever holds a copy.
+struct Sched {
+  int64_t U, u, end;      // units in all, next unit, end of the share
+  int n;
+  // position of unit u
+  int kind, seq, kvh, rt;
+  int64_t item0, items;   // the item's first unit and its units
+  int npt, ntok_all;      // prefix row tiles; tokens of the batch
+  SeqInfo si;
+};
+
+__device__ __forceinline__ void sched_own_item(const PagedGeom& g, const PagedCut& c, Sched& s, int64_t seq0) {
+  const OwnUnits ou = own_units(s.si.qlen, s.si.len, g.prefix, c);
+  const int64_t b = ou.before(s.rt);
+  s.item0 = seq0 + s.kvh * ou.before(ou.nrt) + b;
+  s.items = ou.before(s.rt + 1) - b;
+}
+
+// the first own item of a sequence at or after `seq` that has tokens
+__device__ __forceinline__ void sched_next_seq(const PagedGeom& g, const PagedCut& c, Sched& s, int seq, int64_t u) {
+  for (; seq < g.nseq; ++seq) {
+    s.si = seq_info(g, seq);
+    if (s.si.qlen > 0) break;
+  }
+  s.kind = 1;
+  s.seq = seq;
+  s.kvh = s.rt = 0;
+  if (seq < g.nseq) sched_own_item(g, c, s, u);
+}
+
+struct SchedFound {
+  int seq;
+  int64_t u;  // the sequence's first unit
+};
+// Block-wide (blockDim.x a multiple of 32, at most 1024 threads): total units
+// and the item of the share's first unit.  `red` (33 words) and `found` are in
+// shared memory.
+__device__ __forceinline__ Sched sched_begin(const PagedGeom& g, const PagedCut& c, int64_t* red, SchedFound* found) {
+  const int tid = threadIdx.x, nth = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nth >> 5;
+  Sched s;
+  s.n = gridDim.x;
+  s.ntok_all = batch_tokens(g);
+  s.npt = c.prefix_items ? (s.ntok_all + c.tpt - 1) / c.tpt : 0;
+  const int64_t np = ((int64_t)g.prefix + (1 << c.kt_log2) - 1) >> c.kt_log2;
+  const int64_t PU = (int64_t)s.npt * g.Hkv * np;
+  // units of this thread's run of sequences, and the exclusive sum over the block
+  const int per = (g.nseq + nth - 1) / nth;
+  const int s0 = min(g.nseq, tid * per), s1 = min(g.nseq, s0 + per);
+  int64_t mine = 0;
+  if (c.own_items)
+    for (int q = s0; q < s1; ++q) {
+      const SeqInfo si = seq_info(g, q);
+      if (si.qlen > 0) {
+        const OwnUnits ou = own_units(si.qlen, si.len, g.prefix, c);
+        mine += g.Hkv * ou.before(ou.nrt);
+      }
+    }
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) red[warp] = incl;
+  if (tid == 0) found->seq = g.nseq;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t v = lane < nw ? red[lane] : 0;
+    const int64_t own = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
+    }
+    if (lane < nw) red[lane] = v - own;
+    if (lane == nw - 1) red[32] = v;
+  }
+  __syncthreads();
+  s.U = PU + red[32];
+  s.u = share_begin(s.U, s.n, blockIdx.x);
+  s.end = share_begin(s.U, s.n, blockIdx.x + 1);
+  const int64_t begin = PU + red[warp] + incl - mine;
+  if (s.u < s.end && s.u >= begin && s.u < begin + mine) {
+    int64_t at = begin;
+    for (int q = s0; q < s1; ++q) {
+      const SeqInfo si = seq_info(g, q);
+      if (si.qlen == 0) continue;
+      const OwnUnits ou = own_units(si.qlen, si.len, g.prefix, c);
+      const int64_t n = g.Hkv * ou.before(ou.nrt);
+      if (s.u < at + n) {
+        found->seq = q;
+        found->u = at;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  if (s.u >= s.end) {
+    s.kind = -1;
+    return s;
+  }
+  if (s.u < PU) {
+    s.kind = 0;
+    s.seq = 0;
+    const int64_t item = s.u / np;
+    s.kvh = (int)(item / s.npt);
+    s.rt = (int)(item % s.npt);
+    s.item0 = item * np;
+    s.items = np;
+    return s;
+  }
+  if (found->seq >= g.nseq) {  // the arrays changed under the call
+    s.kind = -1;
+    return s;
+  }
+  s.kind = 1;
+  s.seq = found->seq;
+  s.si = seq_info(g, s.seq);
+  if (s.si.qlen <= 0) {
+    s.kind = -1;
+    return s;
+  }
+  const OwnUnits ou = own_units(s.si.qlen, s.si.len, g.prefix, c);
+  const int64_t per_kvh = ou.before(ou.nrt), x = s.u - found->u;
+  s.kvh = (int)(x / per_kvh);
+  const int64_t y = x % per_kvh;
+  int lo = 0, hi = ou.nrt;  // before(lo) <= y < before(hi)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (ou.before(mid) <= y) lo = mid; else hi = mid;
+  }
+  s.rt = lo;
+  sched_own_item(g, c, s, found->u);
+  return s;
+}
+
+// The next piece of the share (kind -1: none), and the state behind it.
+__device__ __forceinline__ Piece sched_next(const PagedGeom& g, const PagedCut& c, Sched& s) {
+  Piece p;
+  if (s.kind < 0 || s.u >= s.end) {
+    p.kind = -1;
+    return p;
+  }
+  p.kind = s.kind;
+  p.seq = s.seq;
+  p.kvh = s.kvh;
+  p.tile0 = (int)(s.u - s.item0);
+  const int64_t stop = min(s.end, s.item0 + s.items);
+  p.tile1 = (int)(stop - s.item0);
+  p.c0 = share_owner(s.U, s.n, s.item0);
+  p.c1 = share_owner(s.U, s.n, s.item0 + s.items - 1);
+  p.first = p.tile0 == 0;
+  if (s.kind == 0) {
+    p.tok0 = s.rt * c.tpt;
+    p.ntok = min(c.tpt, s.ntok_all - p.tok0);
+    p.off = 0;
+    p.len = g.prefix;
+    p.np = 0;
+  } else {
+    const int t = s.rt * c.tpt;
+    p.tok0 = s.si.q0 + t;
+    p.ntok = min(c.tpt, s.si.qlen - t);
+    p.off = s.si.len - s.si.qlen + t;
+    p.len = p.off + p.ntok;
+    p.np = c.walk_prefix ? (int)(((int64_t)g.prefix + (1 << c.kt_log2) - 1) >> c.kt_log2) : 0;
+  }
+  s.u = stop;
+  if (s.u < s.end) {  // the item is done: the next one
+    const int64_t seq_end_probe = s.item0 + s.items;
+    if (s.kind == 0) {
+      if (++s.rt == s.npt) { s.rt = 0; ++s.kvh; }
+      s.item0 = seq_end_probe;
+      if (s.kvh == g.Hkv) sched_next_seq(g, c, s, 0, seq_end_probe);
+    } else {
+      const OwnUnits ou = own_units(s.si.qlen, s.si.len, g.prefix, c);
+      if (++s.rt == ou.nrt) { s.rt = 0; ++s.kvh; }
+      if (s.kvh == g.Hkv) {
+        sched_next_seq(g, c, s, s.seq + 1, seq_end_probe);
+      } else {
+        s.item0 = seq_end_probe;
+        s.items = ou.before(s.rt + 1) - ou.before(s.rt);
+      }
+    }
+  }
+  return p;
+}
+
+}  // namespace s2o

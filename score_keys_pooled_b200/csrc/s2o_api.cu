@@ -1,6 +1,7 @@
 // C ABI of the S2O library: argument checks, workspace layout and launches.
 // Everything that computes runs in the kernels of pool_score.cuh,
 // seg_sort.cuh and sparse_attn.cuh.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -15,6 +16,9 @@
 #include "sparse_attn2.cuh"
 #include "block_truth.cuh"
 #include "qperm.cuh"
+#include "rotary.cuh"
+#include "paged_sched.cuh"
+#include "paged_attn.cuh"
 
 using namespace s2o;
 
@@ -778,6 +782,7 @@ const char* s2o_status_string(s2o_status st) {
     case S2O_ERR_DEVICE_TIMEOUT: return "bounded device wait ran out";
     case S2O_ERR_NONFINITE: return "non-finite input or score";
     case S2O_ERR_BAD_PLAN: return "plan index out of range";
+    case S2O_ERR_BAD_CACHE: return "page, length or token range out of range";
   }
   return "unknown status";
 }
@@ -791,6 +796,7 @@ s2o_status s2o_last_device_error(s2o_stream_t stream) {
   if (word & kErrTimeout) return S2O_ERR_DEVICE_TIMEOUT;
   if (word & kErrNonFinite) return S2O_ERR_NONFINITE;
   if (word & kErrBadPlan) return S2O_ERR_BAD_PLAN;
+  if (word & kErrBadCache) return S2O_ERR_BAD_CACHE;
   return S2O_OK;
 }
 
@@ -826,3 +832,5 @@ int32_t s2o_last_stage_times(float* ms, const char** names, int32_t cap) {
 }
 
 }  // extern "C"
+
+#include "paged_api.cuh"

@@ -1,0 +1,188 @@
+"""The serving calls without a GPU: the oracle's own pins, every refusal that
+is made before a launch, and the host-side arithmetic of the configs."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import score_keys_pooled_b200 as s2o
+from score_keys_pooled_b200 import build
+from oracle import serve_oracle as SO
+
+GOOD = ctypes.c_void_p(1 << 20)
+ODD = ctypes.c_void_p((1 << 20) + 8)
+
+
+@pytest.fixture(scope="module")
+def L():
+    build.build()
+    return s2o.lib()
+
+
+def cache(**kw):
+    c = dict(Hq=8, Hkv=2, page_size=16, num_pages=10, nseq=2, max_pages=4, Tq=3, max_q=2, prefix_len=20)
+    c.update(kw)
+    return s2o.make_cache(**c)
+
+
+def view(ptr=1 << 20, b=0, t=1024, h=128):
+    return s2o.View(ptr, b, t, h)
+
+
+def test_oracle_rotation_is_complex_multiplication_and_inverts():
+    rng = np.random.default_rng(0)
+    x, pos = rng.standard_normal((5, 3, 128)), np.array([[0, 1, 7, 1000, 12345]])
+    freq = 10000.0 ** (-np.arange(32) / 32.0)
+    y, _ = SO.rotate(x, pos, 64, [0] * 32, freq)
+    z = (x[:, :, :32] + 1j * x[:, :, 32:64]) * np.exp(1j * pos[0][:, None, None] * freq)
+    assert np.allclose(y[:, :, :32], z.real, atol=1e-12) and np.allclose(y[:, :, 32:64], z.imag, atol=1e-12)
+    assert np.array_equal(y[:, :, 64:], x[:, :, 64:]) and np.array_equal(y[0], x[0])
+    assert np.allclose(SO.rotate(y, pos, 64, [0] * 32, freq, inverse=True)[0], x, atol=1e-12)
+
+
+def test_oracle_inverse_is_the_gradient():
+    """<g, d rotate(x)/dx_i> by central differences (the map is linear: exact)."""
+    rng = np.random.default_rng(1)
+    x, g = rng.standard_normal((2, 1, 128)), rng.standard_normal((2, 1, 128))
+    pos = np.array([[3, 900], [5, 1], [0, 77]])
+    r = s2o.make_rotary(96, sections=(12, 18, 18), interleaved=True)
+    turn = lambda y, inv=False: SO.rotate(y, pos, 96, r.axis, r.inv_freq, True, inv)[0]
+    back = turn(g, True)
+    for i in (0, 1, 30, 95, 96, 127):
+        e = np.zeros_like(x)
+        e[:, :, i] = 0.5
+        diff = ((turn(x + e) - turn(x - e)) * g).sum((1, 2))
+        assert np.allclose(diff, back[:, 0, i], atol=1e-12)
+
+
+def test_oracle_attention_is_one_softmax_over_prefix_and_own_keys():
+    rng = np.random.default_rng(2)
+    kc, vc = rng.standard_normal((6, 2, 16, 128)), rng.standard_normal((6, 2, 16, 128))
+    q = rng.standard_normal((3, 4, 128))
+    O, lse, _, _, n = SO.attend(q, kc, vc, np.array([[4, 1]]), [0, 3], [19], [5, 0], 17)
+    k = np.concatenate([kc[5, 1], kc[0, 1, :1], kc[4, 1], kc[1, 1, :2]])  # token 1 sees 17 + 18 of 19 own keys
+    v = np.concatenate([vc[5, 1], vc[0, 1, :1], vc[4, 1], vc[1, 1, :2]])
+    p = np.exp(k @ q[1, 2] / np.sqrt(128))
+    assert list(n) == [34, 35, 36] and np.allclose(lse[1, 2], np.log(p.sum()))
+    assert np.allclose(O[1, 2], p @ v / p.sum())
+
+
+def test_rotary_config_checks():
+    r = s2o.make_rotary(64, theta=500.0, sections=(8, 10, 14))
+    assert list(r.axis[:32]) == [0] * 8 + [1] * 10 + [2] * 14 and r.naxes == 3
+    assert r.inv_freq[5] == 500.0 ** (-10 / 64)
+    for kw in (dict(rot_dim=130), dict(rot_dim=-2), dict(rot_dim=63), dict(sections=(1, 2)),
+               dict(sections=(16, 16, 16, 16)), dict(sections=(65, -1)), dict(inv_freq=[1.0])):
+        with pytest.raises(s2o.S2OError):
+            s2o.make_rotary(**kw)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(Hq=0), 1), (dict(Hkv=3), 1), (dict(nseq=0), 1), (dict(max_pages=0), 1), (dict(num_pages=0), 1),
+    (dict(Tq=-1), 1), (dict(max_q=0), 1), (dict(prefix_len=-1), 1), (dict(dtype=2), 1), (dict(d=64), 2),
+    (dict(page_size=8), 2), (dict(page_size=48), 2), (dict(page_size=256), 2), (dict(Hq=130, Hkv=2), 2),
+    (dict(num_pages=1 << 27, page_size=16), 2), (dict(max_pages=1 << 27), 2), (dict(Tq=1 << 28), 2),
+])
+def test_cache_config_validation(L, change, code):
+    c = cache(**change)
+    n = ctypes.c_size_t(0)
+    assert L.s2o_attention_paged_workspace_size(c, n) == code
+    assert L.s2o_attention_paged(c, GOOD, GOOD, GOOD, GOOD, GOOD, GOOD, GOOD, GOOD, 0, None, GOOD, 1 << 40, None) == code
+    assert L.s2o_cache_append(c, None, None, view(), view(), None, GOOD, GOOD, GOOD, GOOD, GOOD, None, None) == code
+    assert s2o.last_launch_count() == 0
+
+
+def test_attention_paged_refusals(L):
+    c = cache()
+    need = s2o.attention_paged_workspace_size(c)
+    good = [c, GOOD, GOOD, GOOD, GOOD, GOOD, GOOD, GOOD, GOOD, 0, None, GOOD, need, None]
+    for i in (1, 2, 3, 4, 5, 6, 7, 8, 11):
+        assert L.s2o_attention_paged(*(good[:i] + [None] + good[i + 1:])) == 1, i
+    for i in (1, 2, 3, 8, 11):
+        assert L.s2o_attention_paged(*(good[:i] + [ODD] + good[i + 1:])) == 1, i
+    assert L.s2o_attention_paged(*(good[:9] + [2] + good[10:])) == 1
+    assert L.s2o_attention_paged(*(good[:12] + [need - 1, None])) == 3
+    assert L.s2o_attention_paged_workspace_size(c, None) == 1
+    empty = cache(Tq=0)
+    assert L.s2o_attention_paged(*([empty] + good[1:])) == 0 and s2o.last_launch_count() == 0
+
+
+def test_append_refusals(L):
+    c, r = cache(), s2o.make_rotary(128)
+    good = [c, r, view(), view(), view(), None, GOOD, GOOD, GOOD, GOOD, GOOD, view(), None]
+    for i in (2, 3, 4, 6, 7, 8, 9, 10, 11):  # q and q_out come together
+        assert L.s2o_cache_append(*(good[:i] + [None] + good[i + 1:])) == 1, i
+    for i in (9, 10):
+        assert L.s2o_cache_append(*(good[:i] + [ODD] + good[i + 1:])) == 1, i
+    for i in (2, 3, 4, 11):
+        for bad in (view(ptr=(1 << 20) + 2), view(t=1028), view(h=4), view(ptr=0)):
+            assert L.s2o_cache_append(*(good[:i] + [bad] + good[i + 1:])) == 1, i
+    bad = s2o.make_rotary(128)
+    for field, value, code in (("rot_dim", 24, 2), ("rot_dim", 144, 2), ("rot_dim", -16, 1), ("naxes", 0, 1),
+                               ("naxes", 4, 1)):
+        b = s2o.make_rotary(128)
+        setattr(b, field, value)
+        assert L.s2o_cache_append(*(good[:1] + [b] + good[2:])) == code
+    bad.inv_freq[3] = float("nan")
+    assert L.s2o_cache_append(*(good[:1] + [bad] + good[2:])) == 1
+    bad = s2o.make_rotary(128)
+    bad.axis[7] = 1
+    assert L.s2o_cache_append(*(good[:1] + [bad] + good[2:])) == 1
+    assert L.s2o_cache_append(*([cache(Tq=0)] + good[1:])) == 0
+    assert s2o.last_launch_count() == 0
+
+
+def test_rotary_refusals(L):
+    r = s2o.make_rotary(128)
+    good = [r, 0, 1, 4, 2, 1, view(), view(), GOOD, view(), view(), 0, None]
+    for i in (0, 6, 7, 8, 9, 10):
+        assert L.s2o_rotary(*(good[:i] + [None] + good[i + 1:])) == 1, i
+    for i, value in ((1, 2), (2, -1), (3, -1), (4, -1), (5, -1)):
+        assert L.s2o_rotary(*(good[:i] + [value] + good[i + 1:])) == 1, i
+    for i in (6, 7, 9, 10):
+        assert L.s2o_rotary(*(good[:i] + [view(b=12)] + good[i + 1:])) == 1, i
+    assert L.s2o_rotary(*(good[:4] + [5000] + good[5:])) == 2
+    assert L.s2o_rotary(*(good[:3] + [0] + good[4:])) == 0  # nothing to turn
+    assert s2o.last_launch_count() == 0
+
+
+def test_binding_refuses_tensors_the_call_was_not_made_for():
+    c, r = cache(), s2o.make_rotary(128)
+    q, k = torch.zeros(3, 8, 128, dtype=torch.bfloat16), torch.zeros(3, 2, 128, dtype=torch.bfloat16)
+    kc, vc = s2o.alloc_cache(c, "cpu")
+    table, qs, kl = (torch.zeros(s, dtype=torch.int32) for s in ((2, 4), (3,), (2,)))
+    bad = [dict(k=k.half()), dict(k=k[:2]), dict(q=q[:, :4]), dict(v=k.transpose(1, 2)), dict(k_cache=kc[:5]),
+           dict(v_cache=vc.transpose(1, 2)), dict(page_table=table.long()), dict(q_start=qs[:2]),
+           dict(kv_len=kl.float()), dict(positions=torch.zeros(2, 3, dtype=torch.int32)),
+           dict(rotary=None, positions=torch.zeros(1, 3, dtype=torch.int32)), dict(q=None, q_out=q), dict()]
+    for change in bad:  # the last one: right in all but the device
+        a = dict(q=q, k=k, v=k, k_cache=kc, v_cache=vc, page_table=table, q_start=qs, kv_len=kl, rotary=r)
+        a.update(change)
+        with pytest.raises(s2o.S2OError) as e:
+            s2o.cache_append(c, **a)
+        assert e.value.code == 1
+    pre = torch.zeros(2, dtype=torch.int32)
+    for change in (dict(q=q.float()), dict(q=q.transpose(0, 1)), dict(prefix_pages=None), dict(prefix_pages=pre[:1]),
+                   dict(O=q.float()), dict(lse=torch.zeros(3, 7)), dict()):
+        a = dict(q=q, k_cache=kc, v_cache=vc, page_table=table, q_start=qs, kv_len=kl, prefix_pages=pre, O=q,
+                 lse=torch.zeros(3, 8), workspace=torch.zeros(8))
+        a.update(change)
+        with pytest.raises(s2o.S2OError) as e:
+            s2o.attention_paged(c, **a)
+        assert e.value.code == 1
+    x = torch.zeros(1, 3, 8, 128, dtype=torch.bfloat16)
+    pos = torch.zeros(1, 1, 3, dtype=torch.int32)
+    for change in (dict(q=x.float()), dict(q=x[0]), dict(k=x.half()), dict(k=x[:, :2]), dict(positions=pos[0]),
+                   dict(positions=pos.long()), dict(q=x.transpose(2, 3)), dict(q_out=x[:, :, :4]),
+                   dict(q=None, k=None), dict()):
+        a = dict(q=x, k=x, positions=pos)
+        a.update(change)
+        with pytest.raises(s2o.S2OError) as e:
+            s2o.rotary(r, **a)
+        assert e.value.code == 1
+
+
+def test_status_of_a_bad_cache(L):
+    assert s2o.status_string(8) == "page, length or token range out of range"
+    assert s2o.STATUS[8] == "S2O_ERR_BAD_CACHE"
