@@ -63,30 +63,38 @@ int sm_count() {
   return n;
 }
 
-// The paged attention's plan of kernels for a call: a rule on sizes the host
-// knows, so the workspace size and the launches agree.
+// The paged attention's kernels for a call: a rule on sizes the host knows, so
+// the workspace size and the launches agree.
 struct PagedPlan {
-  int R;              // row tiles of 16 of the decode kernel
-  PagedCut cut;
+  bool chunks;   // the tile kernel takes everything: a sequence's new rows fill tiles by themselves
+  bool tiles;    // the tile kernel takes the prefix, the decode kernel the own keys
+  int R;         // row tiles of 16 of the decode kernel
+  PagedCut tile, decode;
 };
 PagedPlan paged_plan(const s2o_cache_config* c) {
-  PagedPlan p;
+  PagedPlan p{};
   const int G = c->Hq / c->Hkv;
-  const int64_t rows = std::max((int64_t)std::min(c->max_q, c->Tq), (int64_t)(c->prefix_len > 0 ? c->Tq : 0)) * G;
+  const int64_t seq_rows = (int64_t)std::min(c->max_q, c->Tq) * G, all_rows = (int64_t)c->Tq * G;
+  p.chunks = seq_rows > 64;
+  p.tiles = !p.chunks && c->prefix_len > 0 && all_rows > 64;
+  p.tile.tpt = 2 * (kLq / G);
+  p.tile.kt_log2 = 7;
+  p.tile.prefix_items = p.tiles;
+  p.tile.own_items = p.tile.walk_prefix = p.chunks;
+  const int64_t rows = !p.tiles && c->prefix_len > 0 ? all_rows : seq_rows;
   p.R = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
   if (16 * p.R < G) p.R = G <= 32 ? 2 : 4;
-  p.cut.tpt = 16 * p.R / G;
-  p.cut.kt_log2 = 6;
-  p.cut.prefix_items = c->prefix_len > 0;
-  p.cut.own_items = 1;
-  p.cut.walk_prefix = 0;
+  p.decode.tpt = 16 * p.R / G;
+  p.decode.kt_log2 = 6;
+  p.decode.prefix_items = c->prefix_len > 0 && !p.tiles;
+  p.decode.own_items = 1;
   return p;
 }
 
 struct PagedWs {
-  int64_t* units;
+  int64_t* units;   // of the tile kernel, of the decode kernel
   int2* meta;
-  PagedPart part;
+  PagedPart tile, decode;
   size_t bytes;
 };
 PagedWs paged_layout(const s2o_cache_config* c, const PagedPlan& p, int n, void* base) {
@@ -100,18 +108,46 @@ PagedWs paged_layout(const s2o_cache_config* c, const PagedPlan& p, int n, void*
   const size_t rows = (size_t)c->Tq * c->Hq;
   w.units = static_cast<int64_t*>(take(256));
   w.meta = static_cast<int2*>(take((size_t)c->Tq * c->Hkv * sizeof(int2)));
-  for (int k = 0; k < 2; ++k) {
-    if (c->prefix_len == 0) continue;  // whole items are the result
-    w.part.dense[k] = static_cast<float*>(take(rows * kD * sizeof(float)));
-    w.part.dense_ml[k] = static_cast<float2*>(take(rows * sizeof(float2)));
-  }
-  w.part.rows = 16 * p.R;
-  w.part.slots = static_cast<float*>(take((size_t)2 * n * w.part.rows * kD * sizeof(float)));
-  w.part.slots_ml = static_cast<float2*>(take((size_t)2 * n * w.part.rows * sizeof(float2)));
+  if (c->prefix_len > 0 && !p.chunks)  // otherwise whole items are the result
+    for (int k = 0; k < 2; ++k) {
+      w.decode.dense[k] = static_cast<float*>(take(rows * kD * sizeof(float)));
+      w.decode.dense_ml[k] = static_cast<float2*>(take(rows * sizeof(float2)));
+    }
+  w.tile = w.decode;
+  auto slots = [&](PagedPart& part, int r) {
+    part.rows = r;
+    part.slots = static_cast<float*>(take((size_t)2 * n * r * kD * sizeof(float)));
+    part.slots_ml = static_cast<float2*>(take((size_t)2 * n * r * sizeof(float2)));
+  };
+  if (p.chunks || p.tiles) slots(w.tile, 2 * kLq);
+  if (!p.chunks) slots(w.decode, 16 * p.R);
   w.bytes = off;
   return w;
 }
 
+// [Tq, Hq, 128] queries as boxes of 64 columns x G heads x `toks` tokens
+bool encode_query_map(CUtensorMap* map, const void* base, int Tq, int Hq, int G, int toks, bool fp16) {
+  EncodeTiledFn enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)Hq, (cuuint64_t)Tq};
+  const cuuint64_t strides[2] = {(cuuint64_t)kD * 2, (cuuint64_t)Hq * kD * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)toks};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool FP16>
+cudaError_t launch_tile(const PagedArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, int n,
+                        cudaStream_t s) {
+  cudaError_t e =
+      cudaFuncSetAttribute(k_paged_tile<FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPtSmem);
+  if (e != cudaSuccess) return e;
+  k_paged_tile<FP16><<<n, kAttn2Threads, kPtSmem, s>>>(a, q, k, v);
+  return cudaGetLastError();
+}
 template <bool FP16, int R>
 cudaError_t launch_decode(const PagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, int n, cudaStream_t s) {
   // the attribute belongs to the function on the current device; setting it
@@ -229,23 +265,38 @@ s2o_status s2o_attention_paged(const s2o_cache_config* cfg, const uint16_t* Q, c
   g.Hq = cfg->Hq; g.Hkv = cfg->Hkv; g.G = cfg->Hq / cfg->Hkv; g.nseq = cfg->nseq; g.max_pages = cfg->max_pages;
   g.num_pages = cfg->num_pages; g.page_log2 = log2_of(cfg->page_size); g.Tq = cfg->Tq; g.max_q = cfg->max_q;
   g.prefix = cfg->prefix_len;
-  a.c = p.cut;
-  a.Q = Q; a.O = O; a.lse = lse; a.part = w.part; a.meta = w.meta; a.units = w.units;
+  a.Q = Q; a.O = O; a.lse = lse; a.meta = w.meta;
   a.out_f32 = out_dtype == S2O_OUT_F32;
-  a.direct = cfg->prefix_len == 0;
-  CUtensorMap tmK, tmV;
+  a.direct = cfg->prefix_len == 0 || p.chunks;
+  CUtensorMap tmQ, tmK, tmV;
   const uint64_t rows = (uint64_t)cfg->num_pages * cfg->Hkv * cfg->page_size;
   const uint32_t box = (uint32_t)std::min(cfg->page_size, 64);
   if (!encode_rows_map(&tmK, k_cache, rows, box) || !encode_rows_map(&tmV, v_cache, rows, box)) return S2O_ERR_CUDA;
   const bool fp16 = cfg->dtype == S2O_TYPE_FP16;
-  if ((fp16 ? launch_decode_r<true>(p.R, a, tmK, tmV, n, s) : launch_decode_r<false>(p.R, a, tmK, tmV, n, s)) !=
-      cudaSuccess)
-    return S2O_ERR_CUDA;
-  ++t_launches;
+  if (p.chunks || p.tiles) {
+    if (!encode_query_map(&tmQ, Q, cfg->Tq, cfg->Hq, g.G, kLq / g.G, fp16)) return S2O_ERR_CUDA;
+    a.c = p.tile;
+    a.part = w.tile;
+    a.units = w.units;
+    if ((fp16 ? launch_tile<true>(a, tmQ, tmK, tmV, n, s) : launch_tile<false>(a, tmQ, tmK, tmV, n, s)) != cudaSuccess)
+      return S2O_ERR_CUDA;
+    ++t_launches;
+  }
+  if (!p.chunks) {
+    a.c = p.decode;
+    a.part = w.decode;
+    a.units = w.units + 1;
+    if ((fp16 ? launch_decode_r<true>(p.R, a, tmK, tmV, n, s) : launch_decode_r<false>(p.R, a, tmK, tmV, n, s)) !=
+        cudaSuccess)
+      return S2O_ERR_CUDA;
+    ++t_launches;
+  }
   JoinArgs j{};
   j.g = g;
-  j.prefix.part = w.part; j.prefix.c = p.cut; j.prefix.units = w.units; j.prefix.n = n; j.prefix.on = cfg->prefix_len > 0;
-  j.own = j.prefix;
+  const JoinSide tile = {w.tile, p.tile, w.units, n, 0}, decode = {w.decode, p.decode, w.units + 1, n, 0};
+  j.prefix = p.tiles ? tile : decode;
+  j.prefix.on = cfg->prefix_len > 0 && !p.chunks;
+  j.own = p.chunks ? tile : decode;
   j.own.on = 1;
   j.meta = w.meta; j.O = O; j.lse = lse; j.out_f32 = a.out_f32;
   const unsigned blocks = (unsigned)(((int64_t)cfg->Tq * cfg->Hq + 7) / 8);

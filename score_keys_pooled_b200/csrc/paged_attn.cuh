@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(PgDecode<R>::kThreads, 1)
   Sched sc = sched_begin(g, a.c, reinterpret_cast<int64_t*>(sgen + C::kOffRed),
                          reinterpret_cast<SchedFound*>(sgen + C::kOffRed + 33 * 8));
   if (tid == 0 && blockIdx.x == 0) *a.units = sc.U;
+  __syncthreads();
   static_assert(sizeof(Piece) <= 64, "piece slot");
   auto piece_at = [&](int k) { return reinterpret_cast<Piece*>(sgen + C::kOffPiece + 64 * k); };
 
@@ -481,16 +482,17 @@ __device__ __forceinline__ void row_add(RowSum& s, float2 ml, float4 o) {
   s.o = make_float4(s.o.x * f + o.x * h, s.o.y * f + o.y * h, s.o.z * f + o.z * h, s.o.w * f + o.w * h);
 }
 __device__ __forceinline__ void side_add(RowSum& s, const JoinSide& d, int kind, size_t row, int tile_row, int c0,
-                                         int c1, int lane) {
+                                         int c1, int stride, int offset, int lane) {
   if (c0 == c1) {
     row_add(s, d.part.dense_ml[kind][row], reinterpret_cast<const float4*>(d.part.dense[kind] + row * kD)[lane]);
     return;
   }
   const int64_t U = *d.units;
+  const int n = d.n / stride;
 #pragma unroll 4
   for (int c = c0; c <= c1; ++c) {
-    if (share_begin(U, d.n, c) == share_begin(U, d.n, c + 1)) continue;  // a share without units
-    const size_t at = (size_t)(2 * c + (c == c0 ? 1 : 0)) * d.part.rows + tile_row;
+    if (share_begin(U, n, c) == share_begin(U, n, c + 1)) continue;  // a share without units
+    const size_t at = (size_t)(2 * (c * stride + offset) + (c == c0 ? 1 : 0)) * d.part.rows + tile_row;
     row_add(s, d.part.slots_ml[at], reinterpret_cast<const float4*>(d.part.slots + at * kD)[lane]);
   }
 }
@@ -516,9 +518,10 @@ __global__ void __launch_bounds__(256) k_paged_join(const __grid_constant__ Join
     const PagedCut& c = a.prefix.c;
     const int npt = (ntok + c.tpt - 1) / c.tpt, rt = t / c.tpt;
     const int64_t np = ((int64_t)g.prefix + (1 << c.kt_log2) - 1) >> c.kt_log2;
-    const int64_t u0 = ((int64_t)kvh * npt + rt) * np, U = *a.prefix.units;
-    side_add(s, a.prefix, 0, row, (t - rt * c.tpt) * g.G + hh, share_owner(U, a.prefix.n, u0),
-             share_owner(U, a.prefix.n, u0 + np - 1), lane);
+    const int team = team_size(c, npt, a.prefix.n), n = a.prefix.n / team;
+    const int64_t u0 = (team > 1 ? (int64_t)kvh : (int64_t)kvh * npt + rt) * np, U = *a.prefix.units;
+    side_add(s, a.prefix, 0, row, (t - rt * c.tpt) * g.G + hh, share_owner(U, n, u0), share_owner(U, n, u0 + np - 1),
+             team, team > 1 ? rt : 0, lane);
   }
   if (a.own.on) {
     int tr = hh;
@@ -526,7 +529,7 @@ __global__ void __launch_bounds__(256) k_paged_join(const __grid_constant__ Join
       const int q0 = g.q_start[seq_of_token(g.q_start, g.nseq, t)];
       tr = max(0, (t - q0) % a.own.c.tpt) * g.G + hh;
     }
-    side_add(s, a.own, 1, row, tr, own.x, own.y, lane);
+    side_add(s, a.own, 1, row, tr, own.x, own.y, 1, 0, lane);
   }
   const float inv = s.l > 0.f ? 1.f / s.l : 0.f;
   if (a.out_f32)

@@ -18,6 +18,10 @@
 // not a whole item leaves its rows' (reference, sum, accumulator) in slot
 // 2c (the item began in an earlier CTA) or 2c + 1 (it began here and goes
 // on), at most one of each per CTA.
+// With prefix items alone and few row tiles (npt <= n / 2) the CTAs work in
+// teams of npt: the members of a team take the same keys for different row
+// tiles at about the same time, so HBM is read once and the others hit L2 (in
+// the plain order every row tile would read the whole prefix from HBM again).
 #pragma once
 
 #include "rotary.cuh"
@@ -135,6 +139,7 @@ struct Sched {
   int kind, seq, kvh, rt;
   int64_t item0, items;   // the item's first unit and its units
   int npt, ntok_all;      // prefix row tiles; tokens of the batch
+  int team;               // CTAs of a team (1: none)
   SeqInfo si;
 };
 
@@ -157,6 +162,11 @@ __device__ __forceinline__ void sched_next_seq(const PagedGeom& g, const PagedCu
   if (seq < g.nseq) sched_own_item(g, c, s, u);
 }
 
+// members of a team; n CTAs then make n / members teams, each with one share
+__device__ __forceinline__ int team_size(const PagedCut& c, int npt, int n) {
+  return c.prefix_items && !c.own_items && npt > 0 && 2 * npt <= n ? npt : 1;
+}
+
 struct SchedFound {
   int seq;
   int64_t u;  // the sequence's first unit
@@ -171,6 +181,21 @@ __device__ __forceinline__ Sched sched_begin(const PagedGeom& g, const PagedCut&
   s.ntok_all = batch_tokens(g);
   s.npt = c.prefix_items ? (s.ntok_all + c.tpt - 1) / c.tpt : 0;
   const int64_t np = ((int64_t)g.prefix + (1 << c.kt_log2) - 1) >> c.kt_log2;
+  s.team = team_size(c, s.npt, s.n);
+  if (s.team > 1) {
+    s.n /= s.team;
+    const int me = blockIdx.x / s.team;
+    s.U = g.Hkv * np;
+    s.kind = me < s.n ? 0 : -1;
+    s.seq = 0;
+    s.u = share_begin(s.U, s.n, me);
+    s.end = share_begin(s.U, s.n, me + 1);
+    s.kvh = (int)(s.u / np);
+    s.rt = blockIdx.x % s.team;
+    s.item0 = s.kvh * np;
+    s.items = np;
+    return s;
+  }
   const int64_t PU = (int64_t)s.npt * g.Hkv * np;
   // units of this thread's run of sequences, and the exclusive sum over the block
   const int per = (g.nseq + nth - 1) / nth;
@@ -277,7 +302,7 @@ __device__ __forceinline__ Piece sched_next(const PagedGeom& g, const PagedCut& 
   p.tile0 = (int)(s.u - s.item0);
   const int64_t stop = min(s.end, s.item0 + s.items);
   p.tile1 = (int)(stop - s.item0);
-  p.c0 = share_owner(s.U, s.n, s.item0);
+  p.c0 = share_owner(s.U, s.n, s.item0);  // team numbers, with teams
   p.c1 = share_owner(s.U, s.n, s.item0 + s.items - 1);
   p.first = p.tile0 == 0;
   if (s.kind == 0) {
@@ -296,18 +321,19 @@ __device__ __forceinline__ Piece sched_next(const PagedGeom& g, const PagedCut& 
   }
   s.u = stop;
   if (s.u < s.end) {  // the item is done: the next one
-    const int64_t seq_end_probe = s.item0 + s.items;
+    const int64_t item_end = s.item0 + s.items;
     if (s.kind == 0) {
-      if (++s.rt == s.npt) { s.rt = 0; ++s.kvh; }
-      s.item0 = seq_end_probe;
-      if (s.kvh == g.Hkv) sched_next_seq(g, c, s, 0, seq_end_probe);
+      if (s.team > 1) ++s.kvh;
+      else if (++s.rt == s.npt) { s.rt = 0; ++s.kvh; }
+      s.item0 = item_end;
+      if (s.kvh == g.Hkv) sched_next_seq(g, c, s, 0, item_end);
     } else {
       const OwnUnits ou = own_units(s.si.qlen, s.si.len, g.prefix, c);
       if (++s.rt == ou.nrt) { s.rt = 0; ++s.kvh; }
       if (s.kvh == g.Hkv) {
-        sched_next_seq(g, c, s, s.seq + 1, seq_end_probe);
+        sched_next_seq(g, c, s, s.seq + 1, item_end);
       } else {
-        s.item0 = seq_end_probe;
+        s.item0 = item_end;
         s.items = ou.before(s.rt + 1) - ou.before(s.rt);
       }
     }

@@ -1,0 +1,475 @@
+// Attention over a paged cache, many query rows a KV head: the shared prefix
+// against the rows of the whole batch, or long chunks of new tokens against
+// the prefix and their own keys.
+//
+// Bound by the tensor core and the exponentials: 256 rows against a key and
+// its value are 4 d * 256 flops for 512 bytes, 256 flops a byte, where HBM
+// stops being the limit.  An item's row tile is therefore 256 rows, two
+// tcgen05 tiles of 128 (G query heads of 128 / G tokens each), that share
+// every K/V tile; roles, tensor-memory layout, chunked softmax and register
+// split are those of k_sparse_attn2 (see there), with these differences:
+//   * keys come from pages: warps 9 and 10 issue TMA boxes (64 columns x
+//     min(page, 64) rows, 128-byte swizzle) into the K and V rings; the last
+//     tile of a list that ends inside it has its missing V rows zeroed in
+//     shared memory before the tensor core may read them (0 * NaN);
+//   * Q tiles are TMA boxes of 64 columns x G heads x 128 / G tokens, fetched
+//     by the head's issuer as soon as the softmax has taken the last scores of
+//     the piece before;
+//   * a CTA walks the pieces of its share (paged_sched.cuh): warp 9 announces
+//     each in a small ring that every role follows, all barriers keep counting
+//     across pieces, and the first P V of a piece waits until the softmax warps
+//     have read the piece before it out of tensor memory;
+//   * a piece that is not the whole answer leaves fp32 accumulators and
+//     (reference, sum) for the join.
+#pragma once
+#include "paged_attn.cuh"
+#include "sparse_attn2.cuh"
+
+namespace s2o {
+
+constexpr int kPtKeys = 128;  // keys of a tile
+constexpr uint32_t kPtOffBar = kOff2V + kStagesV * kTile2Bytes;
+constexpr uint32_t kPtOffPiece = kPtOffBar + 48 * 8;
+constexpr uint32_t kPtOffRed = kPtOffPiece + kPieceSlots * 64;
+constexpr uint32_t kPtSmemData = kPtOffRed + 36 * 8;
+constexpr size_t kPtSmem = kPtSmemData + 1024;
+static_assert(kPtSmem <= 227 * 1024, "shared memory");
+
+// barrier slots; those of k_sparse_attn2 up to the P and O ones
+constexpr int kPtOFree = 23;       // [2] softmax i, one arrive per warp: O_i was read -> issuer i
+constexpr int kPtVTmp = 25;        // V loader's own: boxes of a ragged tile landed
+constexpr int kPtDrain = 26;       // [2]
+constexpr int kPtQFull = 28;       // [2] Q tile i landed -> issuer i
+constexpr int kPtPieceFull = 30;   // [kPieceSlots]
+constexpr int kPtPieceEmpty = 34;  // [kPieceSlots] V loader, 2 issuers, 8 softmax warps
+constexpr int kPtBars = 38;
+constexpr int kPtSlotTmem = 40;
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// tile t of a piece: its page list, first key in it, and the keys the piece's
+// rows can reach there
+struct TileKeys {
+  const int32_t* list;
+  int key0, valid;
+};
+__device__ __forceinline__ TileKeys tile_keys(const PagedGeom& g, const Piece& p, int t) {
+  TileKeys k;
+  if (p.kind == 0 || t < p.np) {
+    k.list = g.prefix_pages;
+    k.key0 = t * kPtKeys;
+    k.valid = min(kPtKeys, g.prefix - k.key0);
+  } else {
+    k.list = g.table + (int64_t)p.seq * g.max_pages;
+    k.key0 = (t - p.np) * kPtKeys;
+    k.valid = min(kPtKeys, p.len - k.key0);
+  }
+  return k;
+}
+
+template <bool FP16>
+__global__ void __launch_bounds__(kAttn2Threads, 1)
+    k_paged_tile(const __grid_constant__ PagedArgs a, const __grid_constant__ CUtensorMap tmQ,
+                 const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* sgen = smem_raw + (sbase - smem_u32(smem_raw));
+  auto bar = [&](int k) { return sbase + kPtOffBar + 8u * (uint32_t)k; };
+  auto piece_at = [&](int k) { return reinterpret_cast<Piece*>(sgen + kPtOffPiece + 64 * k); };
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(sgen + kPtOffBar + 8 * kPtSlotTmem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const PagedGeom& g = a.g;
+  const int tpt = kLq / g.G;      // tokens of a 128-row tile
+  const int trows = tpt * g.G;    // its rows
+
+  if (tid == 0) {
+    for (int k = 0; k < kPtBars; ++k) {
+      uint32_t count = 1;
+      if ((k >= kBarSEmpty && k < kBarSEmpty + 2) || (k >= kBarPFull && k < kBarPFull + 4) ||
+          (k >= kPtOFree && k < kPtOFree + 2))
+        count = 4;
+      if ((k >= kBarKEmpty && k < kBarKEmpty + kStagesK) || (k >= kBarVEmpty && k < kBarVEmpty + kStagesV)) count = 2;
+      if (k >= kPtPieceEmpty) count = 11;
+      mbar_init(bar(k), count);
+    }
+    fence_mbar_init();
+  }
+  // Q rows that no box fills (128 is no multiple of G): zero
+  for (int i = tid; i < (kLq - trows) * 2 * 16; i += kAttn2Threads) {
+    const int row = trows + (i >> 5), qi = (i >> 4) & 1, ch = i & 15;
+    *reinterpret_cast<uint4*>(sgen + kOff2Q + qi * kTile2Bytes + (ch >> 3) * (128 * 128) + swz128(row, ch & 7)) =
+        make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32((const void*)tmem_slot), kTmem2Cols);
+    tmem_relinquish();
+  }
+  Sched sc = sched_begin(g, a.c, reinterpret_cast<int64_t*>(sgen + kPtOffRed),
+                         reinterpret_cast<SchedFound*>(sgen + kPtOffRed + 33 * 8));
+  if (tid == 0 && blockIdx.x == 0) *a.units = sc.U;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // the next piece, for every role but the one that announces them; done: kind < 0
+  auto take_piece = [&](int pi, Piece& p) {
+    const int slot = pi % kPieceSlots;
+    if (!mbar_wait_bounded(bar(kPtPieceFull + slot), (pi / kPieceSlots) & 1)) return false;
+    p = *piece_at(slot);
+    return true;
+  };
+  auto rows_of = [&](const Piece& p, int i) { return max(0, min(tpt, p.ntok - i * tpt)) * g.G; };
+
+  if (warp == kLoadWarp0 || warp == kLoadWarp0 + 1) {
+    // ------------------------------------------------------------------ loaders
+    regs_decrease<kRegsOther>();
+    const bool is_k = warp == kLoadWarp0;
+    const int nst = is_k ? kStagesK : kStagesV;
+    const int bar_full = is_k ? kBarKFull : kBarVFull, bar_empty = is_k ? kBarKEmpty : kBarVEmpty;
+    const uint32_t ring = sbase + (is_k ? kOff2K : kOff2V);
+    const CUtensorMap* tm = is_k ? &tmK : &tmV;
+    const int box_log2 = min(g.page_log2, 6), rest_log2 = g.page_log2 - box_log2;
+    const int bi = lane >> 1, half = lane & 1;  // this lane's box of a tile
+    bool ok = true;
+    uint32_t it = 0, vt = 0;
+    for (int pi = 0; ok; ++pi) {
+      Piece p;
+      if (is_k) {
+        p = sched_next(g, a.c, sc);
+        const int slot = pi % kPieceSlots;
+        if (!warp_ok(mbar_wait_bounded(bar(kPtPieceEmpty + slot), ((pi / kPieceSlots) & 1) ^ 1))) { ok = false; break; }
+        if (lane == 0) {
+          *piece_at(slot) = p;
+          mbar_arrive(bar(kPtPieceFull + slot));
+        }
+        if (p.kind < 0) break;
+        if (p.kind == 1 && p.first)
+          for (int t = lane; t < p.ntok; t += 32) a.meta[(int64_t)(p.tok0 + t) * g.Hkv + p.kvh] = make_int2(p.c0, p.c1);
+      } else {
+        if (!warp_ok(take_piece(pi, p))) { ok = false; break; }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kPtPieceEmpty + pi % kPieceSlots));
+        if (p.kind < 0) break;
+      }
+      // page of this lane's box, one tile ahead
+      auto page_of = [&](int t) {
+        if (t >= p.tile1) return 0;
+        const TileKeys k = tile_keys(g, p, t);
+        if ((bi << box_log2) >= k.valid) return 0;
+        return checked_page(g, k.list, ((k.key0 >> box_log2) + bi) >> rest_log2);
+      };
+      int page_next = page_of(p.tile0);
+      for (int t = p.tile0; t < p.tile1; ++t, ++it) {
+        const int page = page_next;
+        page_next = page_of(t + 1);
+        const TileKeys k = tile_keys(g, p, t);
+        const int nb = (k.valid + (1 << box_log2) - 1) >> box_log2;
+        const int st = it % nst;
+        if (!warp_ok(mbar_wait_bounded(bar(bar_empty + st), ((it / nst) & 1) ^ 1))) { ok = false; break; }
+        const bool ragged = !is_k && k.valid < kPtKeys;
+        const uint32_t full = bar(ragged ? kPtVTmp : bar_full + st);
+        if (lane == 0) mbar_expect_tx(full, (uint32_t)nb << (box_log2 + 8));
+        __syncwarp();
+        if (bi < nb) {
+          const int in_page = (((k.key0 >> box_log2) + bi) & ((1 << rest_log2) - 1)) << box_log2;
+          tma_load_rows(ring + st * kTile2Bytes + half * (128 * 128) + (bi << box_log2) * 128, tm, 64 * half,
+                        ((page * g.Hkv + p.kvh) << g.page_log2) + in_page, full);
+        }
+        if (ragged) {
+          const bool landed = warp_ok(mbar_wait_bounded(full, vt & 1));
+          ++vt;
+          if (!landed) { ok = false; ++it; break; }
+          for (int i = lane; i < (kPtKeys - k.valid) * 16; i += 32) {
+            const int row = k.valid + (i >> 4), ch = i & 15;
+            *reinterpret_cast<uint4*>(sgen + (ring - sbase) + st * kTile2Bytes + (ch >> 3) * (128 * 128) +
+                                      swz128(row, ch & 7)) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(bar_full + st));
+        }
+      }
+    }
+    if (!ok && lane == 0) set_error(kErrTimeout);
+    // nothing may land in shared memory after the CTA ends
+    for (uint32_t k = it > (uint32_t)nst ? it - nst : 0; k < it; ++k)
+      if (!mbar_wait_bounded(bar(bar_full + k % nst), (k / nst) & 1)) {
+        if (lane == 0) set_error(kErrTimeout);
+      }
+  } else if (warp == kMmaWarp || warp == kMmaWarp1) {
+    // ------------------------------------------------------------------ MMA issuers
+    regs_decrease<kRegsOther>();
+    const int i = warp == kMmaWarp ? 0 : 1;
+    if (lane == 0) {
+      constexpr uint32_t kTypes = FP16 ? 0u : (1u << 7) | (1u << 10);
+      const uint32_t idesc_qk = (idesc_bf16_f32(128, kBk, false) & ~((7u << 7) | (7u << 10))) | kTypes;
+      const uint32_t idesc_pv = (idesc_bf16_f32(128, 128, true) & ~((7u << 7) | (7u << 10))) | kTypes;
+      bool ok = true;
+      uint32_t kt = 0;  // tiles so far (K and V rings)
+      uint32_t gc = 0;  // chunks of this head so far
+      uint32_t np = 0;  // pieces this head had rows in
+      uint32_t nq = 0;  // Q tiles asked for
+      auto fetch_q = [&](const Piece& p) {
+        if (p.kind < 0 || rows_of(p, i) == 0) return;
+        mbar_expect_tx(bar(kPtQFull + i), (uint32_t)trows * 256);
+        for (int h = 0; h < 2; ++h)
+          tma_load_3d(sbase + kOff2Q + i * kTile2Bytes + h * (128 * 128), &tmQ, 64 * h, p.kvh * g.G, p.tok0 + i * tpt,
+                      bar(kPtQFull + i));
+        ++nq;
+      };
+      Piece p, next;
+      ok = take_piece(0, next);
+      if (ok) fetch_q(next);
+      for (int pi = 0; ok; ++pi) {
+        p = next;
+        mbar_arrive(bar(kPtPieceEmpty + pi % kPieceSlots));
+        if (p.kind < 0) break;
+        const int ntiles = p.tile1 - p.tile0, nch = 2 * ntiles;
+        if (rows_of(p, i) == 0) {  // let the stages pass
+          for (int t = 0; ok && t < ntiles; ++t) {
+            const uint32_t k = kt + t;
+            ok = mbar_wait_bounded(bar(kBarKFull + k % kStagesK), (k / kStagesK) & 1);
+            if (ok) mbar_arrive(bar(kBarKEmpty + k % kStagesK));
+            if (ok) ok = mbar_wait_bounded(bar(kBarVFull + k % kStagesV), (k / kStagesV) & 1);
+            if (ok) mbar_arrive(bar(kBarVEmpty + k % kStagesV));
+          }
+          kt += ntiles;
+          if (ok) ok = take_piece(pi + 1, next);
+          if (ok) fetch_q(next);
+          continue;
+        }
+        ok = mbar_wait_bounded(bar(kPtQFull + i), np & 1);
+        for (int c = 0; ok && c <= nch; ++c) {
+          if (c < nch) {
+            const int h = c & 1;
+            const uint32_t k = kt + (c >> 1);
+            if (h == 0) {
+              ok = mbar_wait_bounded(bar(kBarKFull + k % kStagesK), (k / kStagesK) & 1);
+              if (!ok) break;
+            }
+            const uint32_t n = gc + c;
+            if (n > 0) {
+              ok = mbar_wait_bounded(bar(kBarSEmpty + i), (n - 1) & 1);
+              if (!ok) break;
+            }
+            tc_fence_after();
+            const uint32_t sQ = sbase + kOff2Q + i * kTile2Bytes;
+            const uint32_t sK = sbase + kOff2K + (k % kStagesK) * kTile2Bytes + kBk * h * 128;
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint64_t ad = sdesc_sw128(sQ + (kk >> 2) * (128 * 128) + (kk & 3) * 32, 16, 1024);
+              const uint64_t bd = sdesc_sw128(sK + (kk >> 2) * (128 * 128) + (kk & 3) * 32, 16, 1024);
+              tc_mma_ss(tmem + col_s(i), ad, bd, idesc_qk, kk > 0 ? 1u : 0u);
+            }
+            tc_commit(bar(kBarSFull + i));
+            if (h == 1) tc_commit(bar(kBarKEmpty + k % kStagesK));
+          }
+          if (c > 0) {
+            const int cp = c - 1, hp = cp & 1;
+            const uint32_t k = kt + (cp >> 1), n = gc + cp;
+            if (hp == 0) {
+              ok = mbar_wait_bounded(bar(kBarVFull + k % kStagesV), (k / kStagesV) & 1);
+              if (!ok) break;
+            }
+            ok = mbar_wait_bounded(bar(kBarPFull + 2 * i + hp), (n >> 1) & 1);
+            if (!ok) break;
+            // the accumulator of the piece before this one has been read
+            if (cp == 0 && np > 0) {
+              ok = mbar_wait_bounded(bar(kPtOFree + i), (np - 1) & 1);
+              if (!ok) break;
+            }
+            if (cp == nch - 1) {  // the softmax took the last scores: Q is free
+              ok = take_piece(pi + 1, next);
+              if (!ok) break;
+              fetch_q(next);
+            }
+            tc_fence_after();
+            const uint32_t sV = sbase + kOff2V + (k % kStagesV) * kTile2Bytes;
+#pragma unroll
+            for (int kk = 0; kk < kBk / 16; ++kk) {
+              const uint64_t bd = sdesc_sw128(sV + (kBk * hp + 16 * kk) * 128, 128 * 128, 1024);
+              tc_mma_ts(tmem + col_o(i), tmem + col_p(i, hp) + 8 * kk, bd, idesc_pv, (cp > 0 || kk > 0) ? 1u : 0u);
+            }
+            tc_commit(bar(kBarODone + 2 * i + hp));
+            if (hp == 1) tc_commit(bar(kBarVEmpty + k % kStagesV));
+          }
+        }
+        kt += ntiles;
+        gc += nch;
+        ++np;
+      }
+      if (!ok) set_error(kErrTimeout);
+      if (nq > 0 && !mbar_wait_bounded(bar(kPtQFull + i), (nq - 1) & 1)) set_error(kErrTimeout);
+      tc_commit(bar(kPtDrain + i));
+      if (!mbar_wait_bounded(bar(kPtDrain + i), 0)) set_error(kErrTimeout);
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax
+    regs_increase<kRegsSoftmax>();
+    constexpr float kShift = FP16 ? 7.f : 0.f;
+    const int qi = warp >> 2;
+    const int r = tid & 127;
+    const int rt = r / g.G, rh = r - rt * g.G;  // token of the tile, head of the group
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + col_s(qi) + lane_base;
+    const uint32_t tO = tmem + col_o(qi) + lane_base;
+    bool ok = true;
+    uint32_t gc = 0;
+    for (int pi = 0; ok; ++pi) {
+      Piece p;
+      if (!warp_ok(take_piece(pi, p))) { ok = false; break; }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kPtPieceEmpty + pi % kPieceSlots));
+      if (p.kind < 0) break;
+      const int rows = rows_of(p, qi);
+      if (rows == 0) continue;
+      const bool has = r < rows;
+      // keys the row sees: of the prefix all, of its own up to itself
+      const int see_own = has ? p.off + qi * tpt + rt + 1 : 0;
+      const int see_pre = has ? g.prefix : 0;
+      float m_run = -INFINITY, ell = 0.f;
+      const int nch = 2 * (p.tile1 - p.tile0);
+      for (int c = 0; ok && c < nch; ++c) {
+        const uint32_t n = gc + c;
+        const int t = p.tile0 + (c >> 1);
+        const bool pre = p.kind == 0 || t < p.np;
+        const int vis = (pre ? see_pre - t * kPtKeys : see_own - (t - p.np) * kPtKeys) - kBk * (c & 1);
+        if (!warp_wait(bar(kBarSFull + qi), n & 1, kSpinLimit)) { ok = false; break; }
+        tc_fence_after();
+        float x[kBk];
+        tmem_ld32(tS, x);
+        tmem_ld32(tS + 32, x + 32);
+        tc_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarSEmpty + qi));
+        const bool full = vis >= kBk;
+        float mt = -INFINITY;
+        if (full) {
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int k = 0; k < kBk; k += 2) m4[(k >> 1) & 3] = fmax3(m4[(k >> 1) & 3], x[k], x[k + 1]);
+          mt = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < kBk; ++k)
+            if (k < vis) mt = fmaxf(mt, x[k]);
+        }
+        mt = fmaf(mt, kPgScale, -kShift);
+        const bool move = mt > m_run + 8.f;
+        float alpha = 1.f;
+        if (move) {
+          alpha = (m_run == -INFINITY) ? 0.f : ex2_approx(m_run - mt);
+          m_run = mt;
+          ell *= alpha;
+        }
+        if (c > 0 && __any_sync(0xffffffffu, move)) {
+          if (!warp_wait(bar(kBarODone + 2 * qi + ((n - 1) & 1)), ((n - 1) >> 1) & 1, kSpinLimit)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int cc = 0; cc < 128; cc += 32) {
+            float o[32];
+            tmem_ld32(tO + cc, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] *= alpha;
+            tmem_st32(tO + cc, o);
+          }
+        }
+        if (full) {
+          const uint64_t s2 = f2_pack(kPgScale, kPgScale), nm2 = f2_pack(-m_run, -m_run);
+          uint64_t rs2 = 0;
+#pragma unroll
+          for (int k = 0; k < kBk; k += 2) {
+            const uint64_t v = f2_fma(f2_pack(x[k], x[k + 1]), s2, nm2);
+            const float p0 = ex2_approx(f2_lo(v)), p1 = ex2_approx(f2_hi(v));
+            rs2 = f2_add(rs2, f2_pack(p0, p1));
+            x[k / 2] = __uint_as_float(pack2<FP16>(p0, p1));
+          }
+          ell += f2_lo(rs2) + f2_hi(rs2);
+        } else {
+          float rs = 0.f;
+#pragma unroll
+          for (int k = 0; k < kBk; k += 2) {
+            const float p0 = (k < vis) ? ex2_approx(fmaf(x[k], kPgScale, -m_run)) : 0.f;
+            const float p1 = (k + 1 < vis) ? ex2_approx(fmaf(x[k + 1], kPgScale, -m_run)) : 0.f;
+            rs += p0 + p1;
+            x[k / 2] = __uint_as_float(pack2<FP16>(p0, p1));
+          }
+          ell += rs;
+        }
+        tmem_st32(tmem + col_p(qi, c & 1) + lane_base, x);
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarPFull + 2 * qi + (c & 1)));
+      }
+      if (ok) {
+        const uint32_t n = gc + nch - 1;
+        ok = warp_wait(bar(kBarODone + 2 * qi + (n & 1)), (n >> 1) & 1, kSpinLimit);
+      }
+      if (!ok) break;
+      gc += nch;
+      tc_fence_after();
+      const bool whole = p.c0 == p.c1, final = whole && a.direct;
+      const float inv = ell == 0.f ? 0.f : 1.f / ell;
+      const size_t orow = (size_t)(p.tok0 + qi * tpt + rt) * g.Hq + p.kvh * g.G + rh;
+      const int sl = 2 * blockIdx.x + (p.first ? 1 : 0);
+      const size_t at = whole ? orow : (size_t)sl * a.part.rows + qi * trows + r;
+      float* part = (whole ? a.part.dense[p.kind] : a.part.slots) + at * kD;
+#pragma unroll
+      for (int cc = 0; cc < 128; cc += 32) {
+        float o[32];
+        tmem_ld32(tO + cc, o);
+        tc_wait_ld();
+        if (!has) {
+        } else if (!final) {
+          float4* dst = reinterpret_cast<float4*>(part + cc);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        } else if (a.out_f32) {
+          float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.O) + orow * kD + cc);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            dst[k] = make_float4(o[4 * k] * inv, o[4 * k + 1] * inv, o[4 * k + 2] * inv, o[4 * k + 3] * inv);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.O) + orow * kD + cc);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            dst[k] = make_uint4(pack2<FP16>(o[8 * k] * inv, o[8 * k + 1] * inv),
+                                pack2<FP16>(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                                pack2<FP16>(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
+                                pack2<FP16>(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kPtOFree + qi));
+      if (has) {
+        if (!final) (whole ? a.part.dense_ml[p.kind] : a.part.slots_ml)[at] = make_float2(m_run, ell);
+        else if (a.lse) a.lse[orow] = lse_of(m_run, ell);
+      }
+    }
+    if (!ok && lane == 0) set_error(kErrTimeout);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmem2Cols);
+  }
+}
+
+}  // namespace s2o

@@ -19,6 +19,7 @@
 #include "rotary.cuh"
 #include "paged_sched.cuh"
 #include "paged_attn.cuh"
+#include "paged_tile.cuh"
 
 using namespace s2o;
 
