@@ -94,6 +94,7 @@ PagedPlan paged_plan(const s2o_cache_config* c) {
 struct PagedWs {
   int64_t* units;   // of the tile kernel, of the decode kernel
   int2* meta;
+  SplitItem* split;
   PagedPart tile, decode;
   size_t bytes;
 };
@@ -107,20 +108,24 @@ PagedWs paged_layout(const s2o_cache_config* c, const PagedPlan& p, int n, void*
   };
   const size_t rows = (size_t)c->Tq * c->Hq;
   w.units = static_cast<int64_t*>(take(256));
-  w.meta = static_cast<int2*>(take((size_t)c->Tq * c->Hkv * sizeof(int2)));
-  if (c->prefix_len > 0 && !p.chunks)  // otherwise whole items are the result
+  const int streams = n * (kPgWarps / p.R);  // workers of the decode kernel
+  if (c->prefix_len == 0 || p.chunks) {  // whole items are the result
+    w.split = static_cast<SplitItem*>(take((size_t)(p.chunks ? n : streams) * sizeof(SplitItem)));
+  } else {
+    w.meta = static_cast<int2*>(take((size_t)c->Tq * c->Hkv * sizeof(int2)));
     for (int k = 0; k < 2; ++k) {
       w.decode.dense[k] = static_cast<float*>(take(rows * kD * sizeof(float)));
       w.decode.dense_ml[k] = static_cast<float2*>(take(rows * sizeof(float2)));
     }
+  }
   w.tile = w.decode;
-  auto slots = [&](PagedPart& part, int r) {
+  auto slots = [&](PagedPart& part, int workers, int r) {
     part.rows = r;
-    part.slots = static_cast<float*>(take((size_t)2 * n * r * kD * sizeof(float)));
-    part.slots_ml = static_cast<float2*>(take((size_t)2 * n * r * sizeof(float2)));
+    part.slots = static_cast<float*>(take((size_t)2 * workers * r * kD * sizeof(float)));
+    part.slots_ml = static_cast<float2*>(take((size_t)2 * workers * r * sizeof(float2)));
   };
-  if (p.chunks || p.tiles) slots(w.tile, 2 * kLq);
-  if (!p.chunks) slots(w.decode, 16 * p.R);
+  if (p.chunks || p.tiles) slots(w.tile, n, 2 * kLq);
+  if (!p.chunks) slots(w.decode, streams, 16 * p.R);
   w.bytes = off;
   return w;
 }
@@ -155,7 +160,7 @@ cudaError_t launch_decode(const PagedArgs& a, const CUtensorMap& k, const CUtens
   cudaError_t e = cudaFuncSetAttribute(k_paged_decode<FP16, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)PgDecode<R>::kSmem);
   if (e != cudaSuccess) return e;
-  k_paged_decode<FP16, R><<<n, PgDecode<R>::kThreads, PgDecode<R>::kSmem, s>>>(a, k, v);
+  k_paged_decode<FP16, R><<<n, 32 * kPgWarps, PgDecode<R>::kSmem, s>>>(a, k, v);
   return cudaGetLastError();
 }
 template <bool FP16>
@@ -265,15 +270,15 @@ s2o_status s2o_attention_paged(const s2o_cache_config* cfg, const uint16_t* Q, c
   g.Hq = cfg->Hq; g.Hkv = cfg->Hkv; g.G = cfg->Hq / cfg->Hkv; g.nseq = cfg->nseq; g.max_pages = cfg->max_pages;
   g.num_pages = cfg->num_pages; g.page_log2 = log2_of(cfg->page_size); g.Tq = cfg->Tq; g.max_q = cfg->max_q;
   g.prefix = cfg->prefix_len;
-  a.Q = Q; a.O = O; a.lse = lse; a.meta = w.meta;
+  a.Q = Q; a.O = O; a.lse = lse; a.meta = w.meta; a.split = w.split;
   a.out_f32 = out_dtype == S2O_OUT_F32;
   a.direct = cfg->prefix_len == 0 || p.chunks;
   CUtensorMap tmQ, tmK, tmV;
   const uint64_t rows = (uint64_t)cfg->num_pages * cfg->Hkv * cfg->page_size;
   const uint32_t box = (uint32_t)std::min(cfg->page_size, 64);
-  if (!encode_rows_map(&tmK, k_cache, rows, box) || !encode_rows_map(&tmV, v_cache, rows, box)) return S2O_ERR_CUDA;
   const bool fp16 = cfg->dtype == S2O_TYPE_FP16;
   if (p.chunks || p.tiles) {
+    if (!encode_rows_map(&tmK, k_cache, rows, box) || !encode_rows_map(&tmV, v_cache, rows, box)) return S2O_ERR_CUDA;
     if (!encode_query_map(&tmQ, Q, cfg->Tq, cfg->Hq, g.G, kLq / g.G, fp16)) return S2O_ERR_CUDA;
     a.c = p.tile;
     a.part = w.tile;
@@ -283,6 +288,8 @@ s2o_status s2o_attention_paged(const s2o_cache_config* cfg, const uint16_t* Q, c
     ++t_launches;
   }
   if (!p.chunks) {
+    if (!encode_rows_map(&tmK, k_cache, rows, kPgSub) || !encode_rows_map(&tmV, v_cache, rows, kPgSub))
+      return S2O_ERR_CUDA;
     a.c = p.decode;
     a.part = w.decode;
     a.units = w.units + 1;
@@ -293,15 +300,20 @@ s2o_status s2o_attention_paged(const s2o_cache_config* cfg, const uint16_t* Q, c
   }
   JoinArgs j{};
   j.g = g;
-  const JoinSide tile = {w.tile, p.tile, w.units, n, 0}, decode = {w.decode, p.decode, w.units + 1, n, 0};
+  const int streams = n * (kPgWarps / p.R);
+  const JoinSide tile = {w.tile, p.tile, w.units, n}, decode = {w.decode, p.decode, w.units + 1, streams};
   j.prefix = p.tiles ? tile : decode;
-  j.prefix.on = cfg->prefix_len > 0 && !p.chunks;
   j.own = p.chunks ? tile : decode;
-  j.own.on = 1;
-  j.meta = w.meta; j.O = O; j.lse = lse; j.out_f32 = a.out_f32;
-  const unsigned blocks = (unsigned)(((int64_t)cfg->Tq * cfg->Hq + 7) / 8);
-  if (fp16) k_paged_join<true><<<blocks, 256, 0, s>>>(j);
-  else k_paged_join<false><<<blocks, 256, 0, s>>>(j);
+  j.meta = w.meta; j.split = w.split; j.O = O; j.lse = lse; j.out_f32 = a.out_f32;
+  if (a.direct) {
+    const dim3 grid(j.own.n, (j.own.part.rows + 31) / 32);
+    if (fp16) k_paged_join_split<true><<<grid, 256, 0, s>>>(j);
+    else k_paged_join_split<false><<<grid, 256, 0, s>>>(j);
+  } else {
+    const unsigned blocks = (unsigned)(((int64_t)cfg->Tq * cfg->Hq + 7) / 8);
+    if (fp16) k_paged_join<true><<<blocks, 256, 0, s>>>(j);
+    else k_paged_join<false><<<blocks, 256, 0, s>>>(j);
+  }
   ++t_launches;
   return launch_status();
 }

@@ -7,20 +7,27 @@
 //
 // Bound by the cache: a key and its value are 512 bytes for 4 d flops a row,
 // 16 flops a byte at 16 rows, far below what the GPU can do, so the kernel is
-// built to keep reads in flight: one CTA per SM, a producer warp that fills a
-// ring of 64-key stages (32 KB each) with TMA tiles of the pages' rows, and
-// consumer warps that turn a stage around in a fraction of the time HBM needs
-// for it.
+// built to keep reads in flight and to have nothing wait for anything else:
 //
-//   * warps: R row tiles of 16 rows (an mma's M) x 4 key slices of 16 keys; a
-//     warp holds its own running reference and sum and a 16 x 128 fp32
-//     accumulator in registers, so a stage needs no exchange between warps;
-//     the four slices are joined once per piece, through shared memory.
+//   * a CTA (one per SM, 8 warps) is 8 / R independent streams of R warps.  A
+//     stream is a worker with a share of its own (paged_sched.cuh): it walks
+//     its keys 16 at a time through its own ring of 8 KB stages (192 KB of
+//     stages per SM), and its first warp issues the TMA boxes itself, each
+//     into the stage that the stream has just read.  A stream costs about 0.4
+//     us of latency per stage and some us per piece (sequence numbers, first
+//     loads, results); the other streams' reads go on meanwhile.  (One ring for
+//     the whole CTA, its 64-key stages cut into 16-key slices over four or
+//     eight warps with a join in shared memory at the end of each piece, spent
+//     8 to 13 us at every piece boundary: 58 and 79 us where this takes what
+//     is noted below.)
+//   * a warp holds 16 query rows (an mma's M), their running reference and
+//     sum, and a 16 x 128 fp32 accumulator in registers; R = 2 or 4 warps of a
+//     stream hold further rows against the same stages.
 //   * products: mma.sync m16n8k16 (bf16 or fp16 in, fp32 out).  With at most
 //     64 rows a KV head the 128-row tcgen05 tile would be mostly empty and
 //     its round trip through tensor memory sits on the latency of a step.
-//   * K and V tiles are TMA boxes (64 columns x min(page, 64) rows) with the
-//     128-byte swizzle, read back by ldmatrix without bank conflicts.
+//   * K and V stages are TMA boxes (64 columns x 16 rows, never across a page)
+//     with the 128-byte swizzle, read back by ldmatrix without bank conflicts.
 //   * P = 2^(s - m) is rounded to the cache's type for the second product (its
 //     matrix instruction has one input type); sums use the unrounded value.
 //     The reference m moves only when the maximum grows by more than 2^8.  In
@@ -35,34 +42,31 @@
 
 namespace s2o {
 
-constexpr int kPgKeys = 64;                        // keys of a stage
-constexpr uint32_t kPgStage = 2 * kPgKeys * 256;   // K then V
-constexpr int kPieceSlots = 4;
+constexpr int kPgKeys = 64;                        // keys of a unit
+constexpr int kPgSub = 16;                         // keys of a stage
+constexpr uint32_t kPgStage = 2 * kPgSub * 256;    // K then V, each two halves of 16 rows x 128 bytes
+constexpr int kPgWarps = 8;
 constexpr float kPgScale = 1.4426950408889634f * 0.08838834764831845f;  // log2(e) / sqrt(128)
 
 template <int R>
 struct PgDecode {
-  static constexpr int kThreads = 128 * R + 32;
-  static constexpr int kStages = R == 4 ? 4 : (R == 2 ? 5 : 6);
-  static constexpr uint32_t kOffJoin = kStages * kPgStage;              // [R][2][16][kJoinPitch] fp32
-  static constexpr uint32_t kJoinPitch = 132;
-  static constexpr uint32_t kOffMl = kOffJoin + R * 2 * 16 * kJoinPitch * 4;  // [R][4][16] float2
-  static constexpr uint32_t kOffPiece = kOffMl + R * 4 * 16 * 8;
-  static constexpr uint32_t kOffBar = kOffPiece + kPieceSlots * 64;
-  static constexpr int kBarFull = 0, kBarEmpty = kStages, kBarPieceFull = 2 * kStages,
-                       kBarPieceEmpty = 2 * kStages + kPieceSlots, kBarJoin = 2 * kStages + 2 * kPieceSlots,
-                       kBars = kBarJoin + R;
-  static constexpr uint32_t kOffRed = kOffBar + 8 * ((kBars + 1) & ~1);
-  static constexpr uint32_t kBytes = kOffRed + 34 * 8 + 16;
+  static constexpr int kStreams = kPgWarps / R;
+  static constexpr int kStages = 3 * R;            // of a stream; 24 in all
+  static constexpr int kPieces = 4 * R;            // piece slots of a stream: more than stages
+  static constexpr uint32_t kOffPiece = kStreams * kStages * kPgStage;
+  static constexpr uint32_t kOffBar = kOffPiece + kStreams * kPieces * 64;
+  static constexpr int kBars = 2 * kStages;        // of a stream: full, empty
+  static constexpr uint32_t kOffRed = kOffBar + kStreams * kBars * 8;
+  static constexpr uint32_t kBytes = kOffRed + 34 * 8 + kPgWarps * sizeof(SchedFound);
   static constexpr size_t kSmem = kBytes + 1024;
 };
 
 // Unfinished rows: fp32 accumulators and (reference, sum), base-2 exponents.
 struct PagedPart {
-  float* dense[2];      // [Tq * Hq, 128]: rows of items that one CTA holds whole (0: prefix, 1: own)
+  float* dense[2];      // [Tq * Hq, 128]: rows of items that one share holds whole (0: prefix, 1: own)
   float2* dense_ml[2];  // [Tq * Hq]
-  float* slots;      // [2 n, rows, 128]
-  float2* slots_ml;  // [2 n, rows]
+  float* slots;      // [2 workers, rows, 128]
+  float2* slots_ml;  // [2 workers, rows]
   int rows;          // rows of a slot
 };
 
@@ -73,7 +77,8 @@ struct PagedArgs {
   void* O;
   float* lse;         // [Tq, Hq] or null
   PagedPart part;
-  int2* meta;         // [Tq, Hkv]: CTAs of the own item a token's rows are in
+  int2* meta;         // [Tq, Hkv]: first and last share of the own item a token's rows are in (join of rows)
+  SplitItem* split;   // [workers] (join of split items)
   int64_t* units;     // total units of this kernel, for the join
   int out_f32;
   int direct;         // whole items are the result (no other list of keys to join)
@@ -133,119 +138,125 @@ __device__ __forceinline__ int checked_page(const PagedGeom& g, const int32_t* l
   return p;
 }
 
+// Where the join finds the rows of an own item.  With the result written
+// directly only split items are joined: one record a CTA, written at the end
+// of its share.
+__device__ __forceinline__ void announce_split(const PagedArgs& a, const Sched& sc, const Piece& p, SplitItem& split,
+                                               int lane) {
+  if (p.kind == 1 && p.first) {
+    const int me = sc.me;
+    const int c1 = p.last ? me : split_end(sc);
+    if (!a.direct) {
+      for (int t = lane; t < p.ntok; t += 32) a.meta[(int64_t)(p.tok0 + t) * a.g.Hkv + p.kvh] = make_int2(me, c1);
+    } else if (!p.last) {
+      split = {p.tok0, p.ntok, p.kvh, c1};
+    }
+  }
+  if (p.kind < 0 && a.direct && lane == 0) a.split[sc.me] = split;
+}
+
 template <bool FP16, int R>
-__global__ void __launch_bounds__(PgDecode<R>::kThreads, 1)
+__global__ void __launch_bounds__(32 * kPgWarps, 1)
     k_paged_decode(const __grid_constant__ PagedArgs a, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV) {
   using C = PgDecode<R>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* sgen = smem_raw + (sbase - smem_u32(smem_raw));
-  auto bar = [&](int k) { return sbase + C::kOffBar + 8u * (uint32_t)k; };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int stream = warp / R, rt = warp % R;
+  const uint32_t ring = sbase + stream * C::kStages * kPgStage;
+  const uint32_t bars = sbase + C::kOffBar + stream * C::kBars * 8;
+  auto full = [&](int st) { return bars + 8u * st; };
+  auto empty = [&](int st) { return bars + 8u * (C::kStages + st); };
+  auto piece_at = [&](uint32_t k) {
+    return reinterpret_cast<Piece*>(sgen + C::kOffPiece + (stream * C::kPieces + k % C::kPieces) * 64);
+  };
+  static_assert(sizeof(Piece) <= 64, "piece slot");
   const PagedGeom& g = a.g;
 
-  if (tid == 0) {
-    for (int k = 0; k < C::kStages; ++k) {
-      mbar_init(bar(C::kBarFull + k), 1);
-      mbar_init(bar(C::kBarEmpty + k), 4 * R);
-    }
-    for (int k = 0; k < kPieceSlots; ++k) {
-      mbar_init(bar(C::kBarPieceFull + k), 1);
-      mbar_init(bar(C::kBarPieceEmpty + k), 4 * R);
-    }
-    for (int k = 0; k < R; ++k) mbar_init(bar(C::kBarJoin + k), 4);
+  if (rt == 0 && lane < C::kStages) {
+    mbar_init(full(lane), 1);
+    mbar_init(empty(lane), R);
     fence_mbar_init();
   }
-  Sched sc = sched_begin(g, a.c, reinterpret_cast<int64_t*>(sgen + C::kOffRed),
-                         reinterpret_cast<SchedFound*>(sgen + C::kOffRed + 33 * 8));
+  Sched sc = sched_begin(g, a.c, C::kStreams, stream, reinterpret_cast<int64_t*>(sgen + C::kOffRed),
+                         reinterpret_cast<SchedFound*>(sgen + C::kOffRed + 34 * 8));
   if (tid == 0 && blockIdx.x == 0) *a.units = sc.U;
   __syncthreads();
-  static_assert(sizeof(Piece) <= 64, "piece slot");
-  auto piece_at = [&](int k) { return reinterpret_cast<Piece*>(sgen + C::kOffPiece + 64 * k); };
 
-  if (warp == 4 * R) {
-    // ------------------------------------------------------------------ producer
-    const int box_log2 = min(g.page_log2, 6);              // rows of a box
-    const int boxes = kPgKeys >> box_log2;                 // of a full stage
-    const int rest_log2 = g.page_log2 - box_log2;          // boxes of a page
-    bool ok = true;
-    uint32_t it = 0;
-    for (int pi = 0; ok; ++pi) {
-      const Piece p = sched_next(g, a.c, sc);
-      const int slot = pi % kPieceSlots;
-      if (!warp_ok(mbar_wait_bounded(bar(C::kBarPieceEmpty + slot), ((pi / kPieceSlots) & 1) ^ 1))) { ok = false; break; }
-      if (lane == 0) {
-        *piece_at(slot) = p;
-        mbar_arrive(bar(C::kBarPieceFull + slot));
-      }
-      if (p.kind < 0) break;
-      if (p.kind == 1 && p.first)  // where the join finds the rows of this item
-        for (int t = lane; t < p.ntok; t += 32) a.meta[(int64_t)(p.tok0 + t) * g.Hkv + p.kvh] = make_int2(p.c0, p.c1);
-      const int32_t* list = p.kind == 0 ? g.prefix_pages : g.table + (int64_t)p.seq * g.max_pages;
-      // boxes of the piece, taken 32 at a time: a lane holds the page of one
-      const int box0 = p.tile0 * boxes, box1 = min(p.tile1 * boxes, (p.len + (1 << box_log2) - 1) >> box_log2);
-      int page = 0, page_next = 0;
-      if (box0 + lane < box1) page_next = checked_page(g, list, (box0 + lane) >> rest_log2);
-      for (int tile = p.tile0; tile < p.tile1; ++tile) {
-        const int b0 = tile * boxes, in32 = (b0 - box0) & 31;
-        if (in32 == 0) {
-          page = page_next;
-          const int nb = b0 + 32 + lane;
-          if (nb < box1) page_next = checked_page(g, list, nb >> rest_log2);
-        }
-        const int st = it % C::kStages;
-        if (!warp_ok(mbar_wait_bounded(bar(C::kBarEmpty + st), ((it / C::kStages) & 1) ^ 1))) { ok = false; break; }
-        const int nb = min(boxes, box1 - b0);
-        if (lane == 0) mbar_expect_tx(bar(C::kBarFull + st), (uint32_t)nb << (box_log2 + 9));
-        __syncwarp();
-        const int i = lane >> 2, half = lane & 1, isv = (lane >> 1) & 1;
-        const int pg = __shfl_sync(0xffffffffu, page, (in32 + i) & 31);
-        if (i < nb) {
-          const int in_page = ((b0 + i) & ((1 << rest_log2) - 1)) << box_log2;
-          const int y = (((pg * g.Hkv + p.kvh) << g.page_log2) + in_page);
-          tma_load_rows(sbase + st * kPgStage + isv * (kPgKeys * 256) + half * (kPgKeys * 128) + ((i << box_log2) * 128),
-                        isv ? &tmV : &tmK, 64 * half, y, bar(C::kBarFull + st));
-        }
-        ++it;
+  // ---- the stream's loads, by its first warp: stage by stage through the
+  // pieces.  A piece's description goes into its slot before the arrival on its
+  // first stage; the end is a piece of kind -1 with a stage that loads nothing.
+  // A piece holds at least one stage, so a slot is read before it comes round.
+  uint32_t put = 0, pieces_put = 0;     // stages and pieces announced
+  int sub = 0, sub1 = 0, base = 0;      // next and last 16 keys of the piece; first of the lanes' pages
+  int page = 0, page_next = 0;          // page of 16 keys base + lane, and of the 32 behind
+  Piece ip;
+  ip.kind = 0;
+  const int32_t* list = nullptr;
+  SplitItem split = {0, 0, 0, 0};
+  const int sub_log2 = g.page_log2 - 4;  // 16-key parts of a page
+  bool ok = true;
+  auto issue = [&]() {
+    if (ip.kind < 0) return;
+    const int st = put % C::kStages;
+    if (R > 1) {  // the other warps have read what was there
+      if (!warp_ok(mbar_wait_bounded(empty(st), ((put / C::kStages) & 1) ^ 1))) {
+        ok = false;
+        return;
       }
     }
-    if (!ok && lane == 0) set_error(kErrTimeout);
-    // nothing may land in shared memory after the CTA ends
-    const uint32_t first = it > (uint32_t)C::kStages ? it - C::kStages : 0;
-    for (uint32_t k = first; k < it; ++k)
-      if (!mbar_wait_bounded(bar(C::kBarFull + k % C::kStages), (k / C::kStages) & 1)) {
-        if (lane == 0) set_error(kErrTimeout);
+    if (sub == sub1) {
+      ip = sched_next(g, a.c, sc);
+      if (lane == 0) *piece_at(pieces_put) = ip;
+      ++pieces_put;
+      announce_split(a, sc, ip, split, lane);
+      if (ip.kind < 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full(st));
+        ++put;
+        return;
       }
-    return;
-  }
-
-  // -------------------------------------------------------------------- consumers
-  const int rt = warp >> 2, ks = warp & 3;
-  const int r0 = lane >> 2, cq = 2 * (lane & 3);
-  float* join = reinterpret_cast<float*>(sgen + C::kOffJoin) + rt * (2 * 16 * C::kJoinPitch);
-  float2* mls = reinterpret_cast<float2*>(sgen + C::kOffMl) + rt * 64;
-  constexpr float kShift = FP16 ? 7.f : 0.f;
-  uint32_t it = 0, jphase = 0;
-  bool ok = true;
-  for (int pi = 0;; ++pi) {
-    const int slot = pi % kPieceSlots;
-    if (!warp_ok(mbar_wait_bounded(bar(C::kBarPieceFull + slot), (pi / kPieceSlots) & 1))) { ok = false; break; }
-    const Piece p = *piece_at(slot);
+      list = ip.kind == 0 ? g.prefix_pages : g.table + (int64_t)ip.seq * g.max_pages;
+      sub = base = ip.tile0 * (kPgKeys / kPgSub);
+      sub1 = (min(ip.len, ip.tile1 * kPgKeys) + kPgSub - 1) / kPgSub;
+      page = sub + lane < sub1 ? checked_page(g, list, (sub + lane) >> sub_log2) : 0;
+      page_next = sub + 32 + lane < sub1 ? checked_page(g, list, (sub + 32 + lane) >> sub_log2) : 0;
+    }
+    if (sub - base == 32) {
+      page = page_next;
+      base = sub;
+      page_next = sub + 32 + lane < sub1 ? checked_page(g, list, (sub + 32 + lane) >> sub_log2) : 0;
+    }
+    const int pg = __shfl_sync(0xffffffffu, page, sub - base);
+    if (lane == 0) mbar_expect_tx(full(st), kPgStage);
     __syncwarp();
-    if (lane == 0) mbar_arrive(bar(C::kBarPieceEmpty + slot));
+    if (lane < 4) {
+      const int half = lane & 1, isv = lane >> 1;
+      const int y = ((pg * g.Hkv + ip.kvh) << g.page_log2) + ((sub & ((1 << sub_log2) - 1)) << 4);
+      tma_load_rows(ring + st * kPgStage + isv * (kPgSub * 256) + half * (kPgSub * 128), isv ? &tmV : &tmK, 64 * half,
+                    y, full(st));
+    }
+    ++sub;
+    ++put;
+  };
+  if (rt == 0)
+    for (int k = 0; k < C::kStages && ok; ++k) issue();
+
+  // ---- the rows
+  const int r0 = lane >> 2, cq = 2 * (lane & 3);
+  constexpr float kShift = FP16 ? 7.f : 0.f;
+  uint32_t it = 0;
+  for (uint32_t pi = 0; ok; ++pi) {
+    if (!warp_ok(mbar_wait_bounded(full(it % C::kStages), (it / C::kStages) & 1))) { ok = false; break; }
+    const Piece p = *piece_at(pi);
     if (p.kind < 0) break;
     const int rows = p.ntok * g.G;
-    if (16 * rt >= rows) {  // no rows: let the stages pass
-      for (int tile = p.tile0; ok && tile < p.tile1; ++tile, ++it) {
-        const int st = it % C::kStages;
-        ok = warp_ok(mbar_wait_bounded(bar(C::kBarFull + st), (it / C::kStages) & 1));
-        if (ok && lane == 0) mbar_arrive(bar(C::kBarEmpty + st));
-      }
-      if (!ok) break;
-      continue;
-    }
-    // this lane's rows: r0 and r0 + 8 of the tile
+    const bool active = 16 * rt < rows;
+    const int sub0 = p.tile0 * (kPgKeys / kPgSub);
+    const int subn = (min(p.len, p.tile1 * kPgKeys) + kPgSub - 1) / kPgSub;
+    // this lane's rows: r0 and r0 + 8 of the warp's 16
     int lim[2];       // keys < lim are seen
     size_t orow[2];   // row of [Tq, Hq]
     bool has[2];
@@ -271,22 +282,24 @@ __global__ void __launch_bounds__(PgDecode<R>::kThreads, 1)
       for (int k = 0; k < 4; ++k) acc[n][k] = 0.f;
     float ref[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
 
-    for (int tile = p.tile0; tile < p.tile1; ++tile, ++it) {
+    for (int t = sub0; t < subn; ++t, ++it) {
       const int st = it % C::kStages;
-      if (!warp_ok(mbar_wait_bounded(bar(C::kBarFull + st), (it / C::kStages) & 1))) { ok = false; break; }
-      const int key0 = tile * kPgKeys + 16 * ks;
-      bool wrote = false;
-      if (key0 < p.len) {
-        const uint32_t sK = sbase + st * kPgStage, sV = sK + kPgKeys * 256;
-        float x[2][4] = {};
+      if (!warp_ok(mbar_wait_bounded(full(st), (it / C::kStages) & 1))) { ok = false; break; }
+      if (active) {
+        const int key0 = t * kPgSub;
+        const uint32_t sK = ring + st * kPgStage, sV = sK + kPgSub * 256;
+        float x[2][4] = {}, y[2][4] = {};  // two chains of products each
         {
-          const uint32_t row = 16 * ks + (lane & 7) + 8 * (lane >> 4);
+          const uint32_t row = (lane & 7) + 8 * (lane >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            uint32_t b[4];
-            ldsm4(sK + (kk >> 2) * (kPgKeys * 128) + swz128(row, 2 * (kk & 3) + ((lane >> 3) & 1)), b);
+          for (int kk = 0; kk < 8; kk += 2) {
+            uint32_t b[4], c[4];
+            ldsm4(sK + (kk >> 2) * (kPgSub * 128) + swz128(row, 2 * (kk & 3) + ((lane >> 3) & 1)), b);
+            ldsm4(sK + (kk >> 2) * (kPgSub * 128) + swz128(row, 2 * (kk & 3) + 2 + ((lane >> 3) & 1)), c);
             mma16816<FP16>(x[0], qf[kk], b[0], b[1]);
             mma16816<FP16>(x[1], qf[kk], b[2], b[3]);
+            mma16816<FP16>(y[0], qf[kk + 1], c[0], c[1]);
+            mma16816<FP16>(y[1], qf[kk + 1], c[2], c[3]);
           }
         }
         // hidden keys, the rows' maxima
@@ -296,7 +309,7 @@ __global__ void __launch_bounds__(PgDecode<R>::kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int key = key0 + 8 * n + cq + (k & 1);
-            x[n][k] = key < lim[k >> 1] ? x[n][k] * kPgScale : -INFINITY;
+            x[n][k] = key < lim[k >> 1] ? (x[n][k] + y[n][k]) * kPgScale : -INFINITY;
             mx[k >> 1] = fmaxf(mx[k >> 1], x[n][k]);
           }
         bool move = false;
@@ -333,137 +346,98 @@ __global__ void __launch_bounds__(PgDecode<R>::kThreads, 1)
             pf[2 * n + 1] = pack2<FP16>(p2, p3);
           }
         }
-        if (key0 + 16 > p.len) {
-          // V rows behind the list: zero (16-byte chunks; the row tiles' warps
-          // of this slice write the same zeros)
-          for (int i = lane; i < 16 * 16; i += 32) {
+        if (key0 + kPgSub > p.len) {
+          // V rows behind the list: zero (the stream's other warps write the
+          // same zeros); before the stage's next TMA write, a proxy fence
+          for (int i = lane; i < kPgSub * 16; i += 32) {
             const int row = i >> 4, ch = i & 15;
             if (key0 + row >= p.len)
-              *reinterpret_cast<uint4*>(sgen + (sV - sbase) + (ch >> 3) * (kPgKeys * 128) +
-                                        swz128(16 * ks + row, ch & 7)) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(sgen + (sV - sbase) + (ch >> 3) * (kPgSub * 128) + swz128(row, ch & 7)) =
+                  make_uint4(0, 0, 0, 0);
           }
-          wrote = true;
+          fence_proxy_async_smem();
           __syncwarp();
         }
         {
-          const uint32_t row = 16 * ks + (lane & 7) + 8 * ((lane >> 3) & 1);
+          const uint32_t row = (lane & 7) + 8 * ((lane >> 3) & 1);
 #pragma unroll
           for (int n = 0; n < 8; ++n) {
             uint32_t b[4];
             const uint32_t ch = 2 * n + (lane >> 4);
-            ldsm4_t(sV + (n >> 2) * (kPgKeys * 128) + swz128(row, ch & 7), b);
+            ldsm4_t(sV + (n >> 2) * (kPgSub * 128) + swz128(row, ch & 7), b);
             mma16816<FP16>(acc[2 * n], pf, b[0], b[1]);
             mma16816<FP16>(acc[2 * n + 1], pf, b[2], b[3]);
           }
         }
       }
-      if (wrote) fence_proxy_async_smem();  // before the stage's next TMA write
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(C::kBarEmpty + st));
+      if (R > 1 && lane == 0) mbar_arrive(empty(st));
+      // the next load into the stage just read; with other warps at it, into
+      // the one before, which they have left by now
+      if (rt == 0 && (R == 1 || it > 0)) issue();
+      if (!ok) break;
     }
     if (!ok) break;
+    if (!active) continue;
 
-    // ---- the four slices of a row tile become one: sums of the lanes, the
-    // common reference, accumulators added pairwise in a fixed order
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 1);
       sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 2);
-      if ((lane & 3) == 0) mls[16 * ks + r0 + 8 * k] = make_float2(ref[k], sum[k]);
     }
-    auto meet = [&]() {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(C::kBarJoin + rt));
-      const bool met = warp_ok(mbar_wait_bounded(bar(C::kBarJoin + rt), jphase));
-      jphase ^= 1;
-      return met;
-    };
-    if (!meet()) { ok = false; break; }
-    float tot[2], top[2];
+    const bool whole = p.first && p.last;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      float2 v[4];
-      top[k] = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        v[w] = mls[16 * w + r0 + 8 * k];
-        top[k] = fmaxf(top[k], v[w].x);
-      }
-      const float m = top[k] == -INFINITY ? 0.f : top[k];
-      tot[k] = 0.f;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) tot[k] += v[w].y * ex2_approx(v[w].x - m);
-      const float f = ex2_approx(ref[k] - m);
-#pragma unroll
-      for (int n = 0; n < 16; ++n) {
-        acc[n][2 * k] *= f;
-        acc[n][2 * k + 1] *= f;
-      }
-    }
-    auto put = [&](float* b) {
-#pragma unroll
-      for (int n = 0; n < 16; ++n) {
-        *reinterpret_cast<float2*>(b + r0 * C::kJoinPitch + 8 * n + cq) = make_float2(acc[n][0], acc[n][1]);
-        *reinterpret_cast<float2*>(b + (r0 + 8) * C::kJoinPitch + 8 * n + cq) = make_float2(acc[n][2], acc[n][3]);
-      }
-    };
-    auto add = [&](const float* b) {
-#pragma unroll
-      for (int n = 0; n < 16; ++n) {
-        const float2 u = *reinterpret_cast<const float2*>(b + r0 * C::kJoinPitch + 8 * n + cq);
-        const float2 v = *reinterpret_cast<const float2*>(b + (r0 + 8) * C::kJoinPitch + 8 * n + cq);
-        acc[n][0] += u.x; acc[n][1] += u.y; acc[n][2] += v.x; acc[n][3] += v.y;
-      }
-    };
-    float* mybuf = join + (ks >> 1) * (16 * C::kJoinPitch);
-    if (ks & 1) put(mybuf);
-    if (!meet()) { ok = false; break; }
-    if (!(ks & 1)) add(mybuf);
-    if (ks == 2) put(mybuf);
-    if (!meet()) { ok = false; break; }
-    if (ks == 0) {
-      add(join + 16 * C::kJoinPitch);
-      const bool whole = p.c0 == p.c1;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if (!has[k]) continue;
-        if (whole && a.direct) {
-          const float inv = tot[k] > 0.f ? 1.f / tot[k] : 0.f;
-#pragma unroll
-          for (int n = 0; n < 16; ++n)
-            store2<FP16>(a.O, a.out_f32, orow[k] * kD + 8 * n + cq, acc[n][2 * k] * inv, acc[n][2 * k + 1] * inv);
-          if (a.lse && (lane & 3) == 0) a.lse[orow[k]] = lse_of(top[k], tot[k]);
-          continue;
-        }
-        const int sl = 2 * blockIdx.x + (p.first ? 1 : 0);
-        const size_t at = whole ? orow[k] : (size_t)sl * a.part.rows + 16 * rt + r0 + 8 * k;
-        float* dst = (whole ? a.part.dense[p.kind] : a.part.slots) + at * kD;
+      if (!has[k]) continue;
+      if (whole && a.direct) {
+        const float inv = sum[k] == 0.f ? 0.f : 1.f / sum[k];
 #pragma unroll
         for (int n = 0; n < 16; ++n)
-          *reinterpret_cast<float2*>(dst + 8 * n + cq) = make_float2(acc[n][2 * k], acc[n][2 * k + 1]);
-        if ((lane & 3) == 0) (whole ? a.part.dense_ml[p.kind] : a.part.slots_ml)[at] = make_float2(top[k], tot[k]);
+          store2<FP16>(a.O, a.out_f32, orow[k] * kD + 8 * n + cq, acc[n][2 * k] * inv, acc[n][2 * k + 1] * inv);
+        if (a.lse && (lane & 3) == 0) a.lse[orow[k]] = lse_of(ref[k], sum[k]);
+        continue;
       }
+      const size_t at =
+          whole ? orow[k] : (size_t)(2 * p.share + (p.first ? 1 : 0)) * a.part.rows + 16 * rt + r0 + 8 * k;
+      float* dst = (whole ? a.part.dense[p.kind] : a.part.slots) + at * kD;
+#pragma unroll
+      for (int n = 0; n < 16; ++n)
+        *reinterpret_cast<float2*>(dst + 8 * n + cq) = make_float2(acc[n][2 * k], acc[n][2 * k + 1]);
+      if ((lane & 3) == 0) (whole ? a.part.dense_ml[p.kind] : a.part.slots_ml)[at] = make_float2(ref[k], sum[k]);
     }
   }
-  if (!ok && lane == 0) set_error(kErrTimeout);
+  if (!ok && lane == 0) {
+    set_error(kErrTimeout);
+    if (a.direct && rt == 0) a.split[stream * gridDim.x + blockIdx.x] = {0, 0, 0, 0};
+  }
+  // nothing may land in shared memory after the CTA ends
+  if (rt == 0)
+    for (uint32_t k = put > (uint32_t)C::kStages ? put - C::kStages : 0; k < put; ++k)
+      if (!mbar_wait_bounded(full(k % C::kStages), (k / C::kStages) & 1)) {
+        if (lane == 0) set_error(kErrTimeout);
+      }
 }
 
 // ---------------------------------------------------------------------------
 // The join: a warp per query row adds the row's parts (the prefix's, then the
-// own keys', each in CTA order, so the result does not depend on timing).
+// own keys', each in share order, so the result does not depend on timing).  The
+// lanes take the (reference, sum) of up to 32 parts at once, agree on the
+// common reference and the weights, then read the accumulators with
+// independent loads: read one by one, each part costs a trip to L2 (23-29 us
+// for 20 parts a row instead of what is noted below).
 
 struct JoinSide {
   PagedPart part;
   PagedCut c;
   const int64_t* units;
-  int n;              // CTAs of the kernel that wrote it
-  int on;
+  int n;              // workers of the kernel that wrote it
 };
 
 struct JoinArgs {
   PagedGeom g;
   JoinSide prefix, own;
   const int2* meta;
+  const SplitItem* split;
   void* O;
   float* lse;
   int out_f32;
@@ -473,65 +447,58 @@ struct RowSum {
   float m, l;
   float4 o;
 };
-__device__ __forceinline__ void row_add(RowSum& s, float2 ml, float4 o) {
-  if (ml.x == -INFINITY && ml.y == 0.f) return;  // saw no key
-  const float m = fmaxf(s.m, ml.x);
-  const float f = ex2_approx(s.m - m), h = ex2_approx(ml.x - m);
-  s.m = m;
-  s.l = s.l * f + ml.y * h;
-  s.o = make_float4(s.o.x * f + o.x * h, s.o.y * f + o.y * h, s.o.z * f + o.z * h, s.o.w * f + o.w * h);
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
 }
-__device__ __forceinline__ void side_add(RowSum& s, const JoinSide& d, int kind, size_t row, int tile_row, int c0,
-                                         int c1, int stride, int offset, int lane) {
-  if (c0 == c1) {
-    row_add(s, d.part.dense_ml[kind][row], reinterpret_cast<const float4*>(d.part.dense[kind] + row * kD)[lane]);
-    return;
-  }
-  const int64_t U = *d.units;
-  const int n = d.n / stride;
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    if (share_begin(U, n, c) == share_begin(U, n, c + 1)) continue;  // a share without units
-    const size_t at = (size_t)(2 * (c * stride + offset) + (c == c0 ? 1 : 0)) * d.part.rows + tile_row;
-    row_add(s, d.part.slots_ml[at], reinterpret_cast<const float4*>(d.part.slots + at * kD)[lane]);
-  }
+__device__ __forceinline__ float warp_add(float x) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
 }
-
-template <bool FP16>
-__global__ void __launch_bounds__(256) k_paged_join(const __grid_constant__ JoinArgs a) {
-  const PagedGeom& g = a.g;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int t = (int)(row / g.Hq), h = (int)(row % g.Hq);
-  const int ntok = batch_tokens(g);
-  if (t >= ntok) return;
-  const int kvh = h / g.G, hh = h - kvh * g.G;
-  RowSum s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-  int2 own = make_int2(0, 0);
-  if (a.own.on) {
-    own = a.meta[(int64_t)t * g.Hkv + kvh];
-    own.x = max(0, min(own.x, a.own.n - 1));  // rows of a refused sequence were never written
-    own.y = max(own.x, min(own.y, a.own.n - 1));
-    if (!a.prefix.on && own.x == own.y) return;  // already the result
-  }
-  if (a.prefix.on) {
-    const PagedCut& c = a.prefix.c;
-    const int npt = (ntok + c.tpt - 1) / c.tpt, rt = t / c.tpt;
-    const int64_t np = ((int64_t)g.prefix + (1 << c.kt_log2) - 1) >> c.kt_log2;
-    const int team = team_size(c, npt, a.prefix.n), n = a.prefix.n / team;
-    const int64_t u0 = (team > 1 ? (int64_t)kvh : (int64_t)kvh * npt + rt) * np, U = *a.prefix.units;
-    side_add(s, a.prefix, 0, row, (t - rt * c.tpt) * g.G + hh, share_owner(U, n, u0), share_owner(U, n, u0 + np - 1),
-             team, team > 1 ? rt : 0, lane);
-  }
-  if (a.own.on) {
-    int tr = hh;
-    if (own.x != own.y) {  // the token's place in its row tile
-      const int q0 = g.q_start[seq_of_token(g.q_start, g.nseq, t)];
-      tr = max(0, (t - q0) % a.own.c.tpt) * g.G + hh;
+// cnt parts; lane l of a batch of 32 has part l's (reference, sum) from
+// ml_of(j, row of the accumulators); a part that saw no key has (-inf, 0)
+template <class F>
+__device__ __forceinline__ void add_parts(RowSum& s, const float* acc, int cnt, int lane, F ml_of) {
+  for (int base = 0; base < cnt; base += 32) {
+    size_t at = 0;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (base + lane < cnt) ml = ml_of(base + lane, at);
+    const float m = fmaxf(s.m, warp_max(ml.x));
+    const float w = ml.x == -INFINITY && ml.y == 0.f ? 0.f : ex2_approx(ml.x - m);
+    const float f = s.m == -INFINITY ? 0.f : ex2_approx(s.m - m);
+    s.m = m;
+    s.l = s.l * f + warp_add(ml.y * w);
+    s.o = make_float4(s.o.x * f, s.o.y * f, s.o.z * f, s.o.w * f);
+    const int n = min(32, cnt - base);
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+      const size_t ak = __shfl_sync(0xffffffffu, at, k);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (wk != 0.f) v = reinterpret_cast<const float4*>(acc + ak * kD)[lane];
+      s.o = make_float4(fmaf(v.x, wk, s.o.x), fmaf(v.y, wk, s.o.y), fmaf(v.z, wk, s.o.z), fmaf(v.w, wk, s.o.w));
     }
-    side_add(s, a.own, 1, row, tr, own.x, own.y, 1, 0, lane);
   }
-  const float inv = s.l > 0.f ? 1.f / s.l : 0.f;
+}
+// parts of shares c0 .. c1; member `offset` of teams of `stride`
+__device__ __forceinline__ void add_split(RowSum& s, const PagedPart& part, int c0, int c1, int stride, int offset,
+                                          int tile_row, int lane) {
+  add_parts(s, part.slots, c1 - c0 + 1, lane, [&](int j, size_t& at) {
+    at = (size_t)(2 * ((c0 + j) * stride + offset) + (j == 0 ? 1 : 0)) * part.rows + tile_row;
+    return part.slots_ml[at];
+  });
+}
+__device__ __forceinline__ void add_dense(RowSum& s, const PagedPart& part, int kind, size_t row, int lane) {
+  add_parts(s, part.dense[kind], 1, lane, [&](int, size_t& at) {
+    at = row;
+    return part.dense_ml[kind][row];
+  });
+}
+template <bool FP16>
+__device__ __forceinline__ void finish_row(const JoinArgs& a, const RowSum& s, size_t row, int lane) {
+  const float inv = s.l == 0.f ? 0.f : 1.f / s.l;
   if (a.out_f32)
     reinterpret_cast<float4*>(static_cast<float*>(a.O) + row * kD)[lane] =
         make_float4(s.o.x * inv, s.o.y * inv, s.o.z * inv, s.o.w * inv);
@@ -539,6 +506,57 @@ __global__ void __launch_bounds__(256) k_paged_join(const __grid_constant__ Join
     reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.O) + row * kD)[lane] =
         make_uint2(pack2<FP16>(s.o.x * inv, s.o.y * inv), pack2<FP16>(s.o.z * inv, s.o.w * inv));
   if (a.lse && lane == 0) a.lse[row] = lse_of(s.m, s.l);
+}
+
+// every row of the batch: its prefix parts and its own
+template <bool FP16>
+__global__ void __launch_bounds__(256) k_paged_join(const __grid_constant__ JoinArgs a) {
+  const PagedGeom& g = a.g;
+  const int lane = threadIdx.x & 31;
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int t = row / g.Hq, h = row - t * g.Hq;
+  if (t >= g.Tq) return;
+  const int ntok = batch_tokens(g);
+  const int kvh = h / g.G, hh = h - kvh * g.G;
+  int2 own = a.meta[(int64_t)t * g.Hkv + kvh];
+  const int64_t PU = *a.prefix.units;
+  if (t >= ntok) return;
+  own.x = max(0, min(own.x, a.own.n - 1));  // rows of a refused sequence were never written
+  own.y = max(own.x, min(own.y, a.own.n - 1));
+  RowSum s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  {
+    const PagedCut& c = a.prefix.c;
+    const int npt = (ntok + c.tpt - 1) / c.tpt, rt = t / c.tpt;
+    const int64_t np = ((int64_t)g.prefix + (1 << c.kt_log2) - 1) >> c.kt_log2;
+    const int team = team_size(c, npt, a.prefix.n), n = shares_of(PU, a.prefix.n / team);
+    const int64_t u0 = (team > 1 ? (int64_t)kvh : (int64_t)kvh * npt + rt) * np;
+    const int c0 = share_owner(PU, n, u0), c1 = share_owner(PU, n, u0 + np - 1);
+    if (c0 == c1) add_dense(s, a.prefix.part, 0, row, lane);
+    else add_split(s, a.prefix.part, c0, c1, team, team > 1 ? rt : 0, (t - rt * c.tpt) * g.G + hh, lane);
+  }
+  if (own.x == own.y) {
+    add_dense(s, a.own.part, 1, row, lane);
+  } else {  // the token's place in its row tile
+    const int q0 = g.q_start[seq_of_token(g.q_start, g.nseq, t)];
+    const int tr = max(0, (t - q0) % a.own.c.tpt) * g.G + hh;
+    add_split(s, a.own.part, own.x, own.y, 1, 0, tr, lane);
+  }
+  finish_row<FP16>(a, s, row, lane);
+}
+
+// own items that two or more workers share (all others are the result already):
+// blocks (c, y) take the rows of the one that begins in share c and goes on
+template <bool FP16>
+__global__ void __launch_bounds__(256) k_paged_join_split(const __grid_constant__ JoinArgs a) {
+  const PagedGeom& g = a.g;
+  const SplitItem it = a.split[blockIdx.x];
+  const int lane = threadIdx.x & 31;
+  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < it.ntok * g.G; r += gridDim.y * 8) {
+    const int t = r / g.G;
+    RowSum s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    add_split(s, a.own.part, blockIdx.x, it.c1, 1, 0, r, lane);
+    finish_row<FP16>(a, s, (size_t)(it.tok0 + t) * g.Hq + it.kvh * g.G + (r - t * g.G), lane);
+  }
 }
 
 }  // namespace s2o

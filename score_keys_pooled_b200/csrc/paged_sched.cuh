@@ -1,4 +1,4 @@
-// How the paged attention's work is cut: items, units and the share of a CTA.
+// How the paged attention's work is cut: items, units and the shares of the workers.
 //
 // An item is a tile of query rows of one KV head against one list of keys.
 // Rows of a tile are ordered token-major: row r is token tok0 + r / G, query
@@ -11,17 +11,20 @@
 //                  prefix keys come first in the same item (long chunks fill
 //                  a tile by themselves, so nothing has to be joined later).
 // A unit is one tile of kt keys of an item.  The U units, in the order prefix
-// items (kvh, row tile), own items (sequence, kvh, row tile), are cut evenly:
-// CTA c of n takes units [c U / n, (c + 1) U / n), so the split follows the
-// actual lengths, which only the device knows, and every CTA reads the same
-// number of key tiles.  A CTA's part of an item is a piece; a piece that is
-// not a whole item leaves its rows' (reference, sum, accumulator) in slot
-// 2c (the item began in an earlier CTA) or 2c + 1 (it began here and goes
-// on), at most one of each per CTA.
-// With prefix items alone and few row tiles (npt <= n / 2) the CTAs work in
+// items (kvh, row tile), own items (sequence, kvh, row tile), are cut into n
+// even shares: share c takes units [c U / n, (c + 1) U / n), so the split
+// follows the actual lengths, which only the device knows, and every share
+// reads the same number of key tiles (n is the kernel's number of workers, or
+// U where that is less).  A share's part of an item is a piece; a piece that
+// is not a whole item leaves its rows' (reference, sum, accumulator) in slot
+// 2c (the item began in an earlier share) or 2c + 1 (it began here and goes
+// on), at most one of each per share.
+// With prefix items alone and few row tiles (npt <= n / 2) the workers form
 // teams of npt: the members of a team take the same keys for different row
 // tiles at about the same time, so HBM is read once and the others hit L2 (in
 // the plain order every row tile would read the whole prefix from HBM again).
+// A share is then a team's, and a member's slots are those of share * npt +
+// member.
 #pragma once
 
 #include "rotary.cuh"
@@ -70,16 +73,31 @@ __device__ __forceinline__ SeqInfo seq_info(const PagedGeom& g, int s) {
 // tokens of the batch: rows behind the last sequence belong to nobody
 __device__ __forceinline__ int batch_tokens(const PagedGeom& g) { return max(0, min(g.q_start[g.nseq], g.Tq)); }
 
+// a / b, a >= 0, b > 0: the 64-bit division is a long subroutine, so numbers
+// that fit take the 32-bit one (a piece's bookkeeping sits between two loads)
+__host__ __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+  return a / b;
+}
+
 // sum over i < n of floor((a i + b) / m), n, a, b >= 0, m > 0
 __host__ __device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
   int64_t r = 0;
   while (n > 0) {
-    if (a >= m) { r += n * (n - 1) / 2 * (a / m); a %= m; }
-    if (b >= m) { r += n * (b / m); b %= m; }
+    if (a >= m) {
+      const int64_t q = quot(a, m);
+      r += n * (n - 1) / 2 * q;
+      a -= q * m;
+    }
+    if (b >= m) {
+      const int64_t q = quot(b, m);
+      r += n * q;
+      b -= q * m;
+    }
     const int64_t y = a * n + b;
     if (y < m) break;
-    n = y / m;
-    b = y % m;
+    n = quot(y, m);
+    b = y - n * m;
     const int64_t t = m; m = a; a = t;
   }
   return r;
@@ -94,6 +112,7 @@ struct OwnUnits {
   __host__ __device__ int64_t before(int rt) const {
     if (rt <= 0) return 0;
     const int64_t kt = (int64_t)1 << kt_log2;
+    if (nrt == 1) return np + ((len + kt - 1) >> kt_log2);
     int64_t u = (int64_t)rt * np + floor_sum(rt < nrt ? rt : rt - 1, kt, tpt, (int64_t)off + tpt + kt - 1);
     if (rt >= nrt) u += (len + kt - 1) >> kt_log2;
     return u;
@@ -102,7 +121,7 @@ struct OwnUnits {
 
 __host__ __device__ __forceinline__ OwnUnits own_units(int qlen, int len, int prefix, const PagedCut& c) {
   OwnUnits u;
-  u.nrt = (qlen + c.tpt - 1) / c.tpt;
+  u.nrt = qlen <= c.tpt ? 1 : (qlen + c.tpt - 1) / c.tpt;
   u.np = c.walk_prefix ? (int)(((int64_t)prefix + (1 << c.kt_log2) - 1) >> c.kt_log2) : 0;
   u.len = len;
   u.off = len - qlen;
@@ -111,13 +130,14 @@ __host__ __device__ __forceinline__ OwnUnits own_units(int qlen, int len, int pr
   return u;
 }
 
-__host__ __device__ __forceinline__ int64_t share_begin(int64_t U, int n, int c) { return U * c / n; }
-// the CTA whose share holds unit u
+__host__ __device__ __forceinline__ int shares_of(int64_t U, int workers) { return U < workers ? (int)U : workers; }
+__host__ __device__ __forceinline__ int64_t share_begin(int64_t U, int n, int c) { return quot(U * c, n); }
+// the share that holds unit u
 __host__ __device__ __forceinline__ int share_owner(int64_t U, int n, int64_t u) {
-  return (int)(((u + 1) * n - 1) / U);
+  return (int)quot((u + 1) * n - 1, U);
 }
 
-// A piece: the CTA's part of an item.
+// A piece: the share's part of an item.
 struct Piece {
   int kind;          // 0 prefix item, 1 own item, -1 no more
   int seq, kvh;
@@ -126,20 +146,19 @@ struct Piece {
   int len;           // keys of the list the rows of the tile can reach (prefix: all of it)
   int np;            // leading tiles that are the prefix's
   int tile0, tile1;  // tiles of the item the piece covers
-  int c0, c1;        // CTAs that hold the item's first and last unit
-  int first;         // the piece begins the item
+  int first, last;   // the piece begins, ends the item
+  int share;         // number of the worker (its slots)
 };
 
-// Walks the pieces of a CTA's share.  All threads of a block call
-// `sched_begin` once; the state is then advanced by whoever holds a copy.
+// Walks the pieces of a share.
 struct Sched {
   int64_t U, u, end;      // units in all, next unit, end of the share
-  int n;
+  int n, me;              // shares; this one
   // position of unit u
   int kind, seq, kvh, rt;
   int64_t item0, items;   // the item's first unit and its units
   int npt, ntok_all;      // prefix row tiles; tokens of the batch
-  int team;               // CTAs of a team (1: none)
+  int team;               // members of a team (1: none)
   SeqInfo si;
 };
 
@@ -162,7 +181,7 @@ __device__ __forceinline__ void sched_next_seq(const PagedGeom& g, const PagedCu
   if (seq < g.nseq) sched_own_item(g, c, s, u);
 }
 
-// members of a team; n CTAs then make n / members teams, each with one share
+// members of a team of n workers
 __device__ __forceinline__ int team_size(const PagedCut& c, int npt, int n) {
   return c.prefix_items && !c.own_items && npt > 0 && 2 * npt <= n ? npt : 1;
 }
@@ -172,26 +191,30 @@ struct SchedFound {
   int64_t u;  // the sequence's first unit
 };
 // Block-wide (blockDim.x a multiple of 32, at most 1024 threads): total units
-// and the item of the share's first unit.  `red` (33 words) and `found` are in
-// shared memory.
-__device__ __forceinline__ Sched sched_begin(const PagedGeom& g, const PagedCut& c, int64_t* red, SchedFound* found) {
+// and the item of the first unit of this thread's share.  A block is `own`
+// workers (1 to 8), worker w of block b is number w * gridDim.x + b; the
+// calling thread asks for worker `which` of its block.  `red` (33 words) and `found` (`own`
+// entries) are in shared memory.
+__device__ __forceinline__ Sched sched_begin(const PagedGeom& g, const PagedCut& c, int own, int which, int64_t* red,
+                                             SchedFound* found) {
   const int tid = threadIdx.x, nth = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nth >> 5;
   Sched s;
-  s.n = gridDim.x;
+  const int workers = gridDim.x * own, number = which * gridDim.x + blockIdx.x;
   s.ntok_all = batch_tokens(g);
   s.npt = c.prefix_items ? (s.ntok_all + c.tpt - 1) / c.tpt : 0;
   const int64_t np = ((int64_t)g.prefix + (1 << c.kt_log2) - 1) >> c.kt_log2;
-  s.team = team_size(c, s.npt, s.n);
+  s.team = team_size(c, s.npt, workers);
   if (s.team > 1) {
-    s.n /= s.team;
-    const int me = blockIdx.x / s.team;
     s.U = g.Hkv * np;
-    s.kind = me < s.n ? 0 : -1;
+    s.n = shares_of(s.U, workers / s.team);
+    s.me = number / s.team;
+    s.kind = s.me < s.n ? 0 : -1;
     s.seq = 0;
-    s.u = share_begin(s.U, s.n, me);
-    s.end = share_begin(s.U, s.n, me + 1);
-    s.kvh = (int)(s.u / np);
-    s.rt = blockIdx.x % s.team;
+    if (s.kind < 0) return s;
+    s.u = share_begin(s.U, s.n, s.me);
+    s.end = share_begin(s.U, s.n, s.me + 1);
+    s.kvh = (int)quot(s.u, np);
+    s.rt = number - s.me * s.team;
     s.item0 = s.kvh * np;
     s.items = np;
     return s;
@@ -216,7 +239,7 @@ __device__ __forceinline__ Sched sched_begin(const PagedGeom& g, const PagedCut&
     if (lane >= o) incl += y;
   }
   if (lane == 31) red[warp] = incl;
-  if (tid == 0) found->seq = g.nseq;
+  if (tid < own) found[tid].seq = g.nseq;
   __syncthreads();
   if (warp == 0) {
     int64_t v = lane < nw ? red[lane] : 0;
@@ -231,63 +254,78 @@ __device__ __forceinline__ Sched sched_begin(const PagedGeom& g, const PagedCut&
   }
   __syncthreads();
   s.U = PU + red[32];
-  s.u = share_begin(s.U, s.n, blockIdx.x);
-  s.end = share_begin(s.U, s.n, blockIdx.x + 1);
+  s.n = shares_of(s.U, workers);
+  s.me = number;
   const int64_t begin = PU + red[warp] + incl - mine;
-  if (s.u < s.end && s.u >= begin && s.u < begin + mine) {
+  // the thread whose sequences hold a worker's first unit looks it up
+  for (int w = 0; w < own && mine > 0; ++w) {
+    const int me = w * gridDim.x + blockIdx.x;
+    if (me >= s.n) break;
+    const int64_t u = share_begin(s.U, s.n, me);
+    if (u < begin || u >= begin + mine) continue;
     int64_t at = begin;
     for (int q = s0; q < s1; ++q) {
       const SeqInfo si = seq_info(g, q);
       if (si.qlen == 0) continue;
       const OwnUnits ou = own_units(si.qlen, si.len, g.prefix, c);
       const int64_t n = g.Hkv * ou.before(ou.nrt);
-      if (s.u < at + n) {
-        found->seq = q;
-        found->u = at;
+      if (u < at + n) {
+        found[w].seq = q;
+        found[w].u = at;
         break;
       }
       at += n;
     }
   }
   __syncthreads();
-  if (s.u >= s.end) {
+  if (s.me >= s.n) {
     s.kind = -1;
     return s;
   }
+  s.u = share_begin(s.U, s.n, s.me);
+  s.end = share_begin(s.U, s.n, s.me + 1);
   if (s.u < PU) {
     s.kind = 0;
     s.seq = 0;
-    const int64_t item = s.u / np;
-    s.kvh = (int)(item / s.npt);
-    s.rt = (int)(item % s.npt);
+    const int64_t item = quot(s.u, np);
+    s.kvh = (int)quot(item, s.npt);
+    s.rt = (int)(item - (int64_t)s.kvh * s.npt);
     s.item0 = item * np;
     s.items = np;
     return s;
   }
-  if (found->seq >= g.nseq) {  // the arrays changed under the call
+  if (found[which].seq >= g.nseq) {  // the arrays changed under the call
     s.kind = -1;
     return s;
   }
   s.kind = 1;
-  s.seq = found->seq;
+  s.seq = found[which].seq;
   s.si = seq_info(g, s.seq);
   if (s.si.qlen <= 0) {
     s.kind = -1;
     return s;
   }
   const OwnUnits ou = own_units(s.si.qlen, s.si.len, g.prefix, c);
-  const int64_t per_kvh = ou.before(ou.nrt), x = s.u - found->u;
-  s.kvh = (int)(x / per_kvh);
-  const int64_t y = x % per_kvh;
+  const int64_t per_kvh = ou.before(ou.nrt), x = s.u - found[which].u;
+  s.kvh = (int)quot(x, per_kvh);
+  const int64_t y = x - s.kvh * per_kvh;
   int lo = 0, hi = ou.nrt;  // before(lo) <= y < before(hi)
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (ou.before(mid) <= y) lo = mid; else hi = mid;
   }
   s.rt = lo;
-  sched_own_item(g, c, s, found->u);
+  sched_own_item(g, c, s, found[which].u);
   return s;
 }
+
+// An own item that begins in a share and goes on: what the join of split items
+// reads, one of each worker (ntok 0: none).
+struct SplitItem {
+  int tok0, ntok, kvh, c1;
+};
+// the share that holds the last unit of the item a share ends in
+__device__ __forceinline__ int split_end(const Sched& s) { return share_owner(s.U, s.n, s.item0 + s.items - 1); }
 
 // The next piece of the share (kind -1: none), and the state behind it.
 __device__ __forceinline__ Piece sched_next(const PagedGeom& g, const PagedCut& c, Sched& s) {
@@ -297,14 +335,14 @@ __device__ __forceinline__ Piece sched_next(const PagedGeom& g, const PagedCut& 
     return p;
   }
   p.kind = s.kind;
+  p.share = s.team > 1 ? s.me * s.team + s.rt : s.me;
   p.seq = s.seq;
   p.kvh = s.kvh;
   p.tile0 = (int)(s.u - s.item0);
   const int64_t stop = min(s.end, s.item0 + s.items);
   p.tile1 = (int)(stop - s.item0);
-  p.c0 = share_owner(s.U, s.n, s.item0);  // team numbers, with teams
-  p.c1 = share_owner(s.U, s.n, s.item0 + s.items - 1);
   p.first = p.tile0 == 0;
+  p.last = p.tile1 == s.items;
   if (s.kind == 0) {
     p.tok0 = s.rt * c.tpt;
     p.ntok = min(c.tpt, s.ntok_all - p.tok0);

@@ -28,6 +28,7 @@
 namespace s2o {
 
 constexpr int kPtKeys = 128;  // keys of a tile
+constexpr int kPieceSlots = 4;
 constexpr uint32_t kPtOffBar = kOff2V + kStagesV * kTile2Bytes;
 constexpr uint32_t kPtOffPiece = kPtOffBar + 48 * 8;
 constexpr uint32_t kPtOffRed = kPtOffPiece + kPieceSlots * 64;
@@ -111,8 +112,8 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
     tmem_alloc(smem_u32((const void*)tmem_slot), kTmem2Cols);
     tmem_relinquish();
   }
-  Sched sc = sched_begin(g, a.c, reinterpret_cast<int64_t*>(sgen + kPtOffRed),
-                         reinterpret_cast<SchedFound*>(sgen + kPtOffRed + 33 * 8));
+  Sched sc = sched_begin(g, a.c, 1, 0, reinterpret_cast<int64_t*>(sgen + kPtOffRed),
+                         reinterpret_cast<SchedFound*>(sgen + kPtOffRed + 34 * 8));
   if (tid == 0 && blockIdx.x == 0) *a.units = sc.U;
   tc_fence_before();
   __syncthreads();
@@ -140,6 +141,7 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
     const int bi = lane >> 1, half = lane & 1;  // this lane's box of a tile
     bool ok = true;
     uint32_t it = 0, vt = 0;
+    SplitItem split = {0, 0, 0, 0};
     for (int pi = 0; ok; ++pi) {
       Piece p;
       if (is_k) {
@@ -150,9 +152,8 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
           *piece_at(slot) = p;
           mbar_arrive(bar(kPtPieceFull + slot));
         }
+        announce_split(a, sc, p, split, lane);
         if (p.kind < 0) break;
-        if (p.kind == 1 && p.first)
-          for (int t = lane; t < p.ntok; t += 32) a.meta[(int64_t)(p.tok0 + t) * g.Hkv + p.kvh] = make_int2(p.c0, p.c1);
       } else {
         if (!warp_ok(take_piece(pi, p))) { ok = false; break; }
         __syncwarp();
@@ -198,7 +199,10 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
         }
       }
     }
-    if (!ok && lane == 0) set_error(kErrTimeout);
+    if (!ok && lane == 0) {
+      set_error(kErrTimeout);
+      if (a.direct && is_k) a.split[blockIdx.x] = {0, 0, 0, 0};
+    }
     // nothing may land in shared memory after the CTA ends
     for (uint32_t k = it > (uint32_t)nst ? it - nst : 0; k < it; ++k)
       if (!mbar_wait_bounded(bar(bar_full + k % nst), (k / nst) & 1)) {
@@ -422,10 +426,10 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
       if (!ok) break;
       gc += nch;
       tc_fence_after();
-      const bool whole = p.c0 == p.c1, final = whole && a.direct;
+      const bool whole = p.first && p.last, final = whole && a.direct;
       const float inv = ell == 0.f ? 0.f : 1.f / ell;
       const size_t orow = (size_t)(p.tok0 + qi * tpt + rt) * g.Hq + p.kvh * g.G + rh;
-      const int sl = 2 * blockIdx.x + (p.first ? 1 : 0);
+      const int sl = 2 * p.share + (p.first ? 1 : 0);
       const size_t at = whole ? orow : (size_t)sl * a.part.rows + qi * trows + r;
       float* part = (whole ? a.part.dense[p.kind] : a.part.slots) + at * kD;
 #pragma unroll
