@@ -344,37 +344,47 @@ def _refuse(what: str):
     raise S2OError(1, what)
 
 
-def _view3(t, what, H, T, dtype, device):
+def _wrong(t, what, shape, dtype, device, layout):
+    _refuse(f"{what}: want a {dtype} {list(shape)} tensor with {layout} on {device}, "
+            f"got {t.dtype} {list(t.shape)} strides {t.stride()} on {t.device}")
+
+
+def _view3(t, what, shape, dtype, device):
     """[T, H, 128] with contiguous rows."""
-    if t.dtype != dtype or t.device != device or t.shape != (T, H, 128) or (t.stride(2) != 1 and t.numel()):
-        _refuse(f"{what}: want a {dtype} [{T}, {H}, 128] tensor with contiguous rows on {device}, "
-                f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
-    return View(t.data_ptr(), 0, t.stride(0), t.stride(1))
+    if t.dtype is not dtype or t.device != device or t.shape != shape:
+        _wrong(t, what, shape, dtype, device, "contiguous rows")
+    st, sh, one = t.stride()
+    if one != 1 and t.numel():
+        _wrong(t, what, shape, dtype, device, "contiguous rows")
+    return View(t.data_ptr(), 0, st, sh)
 
 
-def _view4(t, what, B, N, H, dtype, device):
+def _view4(t, what, shape, dtype, device):
     """[B, N, H, 128] with contiguous rows."""
-    if t.dtype != dtype or t.device != device or t.shape != (B, N, H, 128) or (t.stride(3) != 1 and t.numel()):
-        _refuse(f"{what}: want a {dtype} [{B}, {N}, {H}, 128] tensor with contiguous rows on {device}, "
-                f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
-    return View(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+    if t.dtype is not dtype or t.device != device or t.shape != shape:
+        _wrong(t, what, shape, dtype, device, "contiguous rows")
+    sb, st, sh, one = t.stride()
+    if one != 1 and t.numel():
+        _wrong(t, what, shape, dtype, device, "contiguous rows")
+    return View(t.data_ptr(), sb, st, sh)
 
 
 def _plain(t, what, shape, dtype, device):
     """A contiguous tensor of this shape."""
-    if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
-        _refuse(f"{what}: want a contiguous {dtype} tensor of {tuple(shape)} on {device}, "
-                f"got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+    if t.dtype is not dtype or t.device != device or t.shape != shape or not t.is_contiguous():
+        _wrong(t, what, shape, dtype, device, "no gaps")
     return t.data_ptr()
 
 
-def _empty(shape, dtype, device, stream):
+def _empty(shape, dtype, device, stream, strides=None):
     """Memory that belongs to the stream it is used on."""
     import torch
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _empty(shape, dtype, device, None, strides)
+    if strides is not None:
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+    return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _call_on(device, stream, fn, name, *args):
@@ -382,11 +392,12 @@ def _call_on(device, stream, fn, name, *args):
     import torch
     if device.type != "cuda":
         _refuse(f"{name}: the tensors are on {device}, not on a CUDA device")
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, (stream or torch.cuda.current_stream(device)).cuda_stream), name)
-    else:
+    if device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
-            _check(fn(*args, (stream or torch.cuda.current_stream(device)).cuda_stream), name)
+            return _call_on(device, stream, fn, name, *args)
+    code = fn(*args, (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream)
+    if code:
+        raise S2OError(code, name)
 
 
 def rotary(r: RotaryConfig, q, k, positions, q_out=None, k_out=None, inverse: bool = False, stream=None):
@@ -403,18 +414,18 @@ def rotary(r: RotaryConfig, q, k, positions, q_out=None, k_out=None, inverse: bo
     if t is not torch.bfloat16 and t is not torch.float16:
         _refuse(f"rotary: {t} is neither bfloat16 nor float16")
     sides = []
-    for name, src, dst in (("q", q, q_out), ("k", k, k_out)):
+    for name, src, dst in (("rotary: q", q, q_out), ("rotary: k", k, k_out)):
         if src is None:
             sides.append((0, None, None, None))
             continue
         if src.dim() != 4:
-            _refuse(f"rotary: {name} must be a [B, N, H, 128] tensor")
+            _refuse(f"{name} must be a [B, N, H, 128] tensor")
         H = src.shape[2]
-        vin = _view4(src, "rotary: " + name, B, N, H, t, dev)
+        shape = (B, N, H, 128)
+        vin = _view4(src, name, shape, t, dev)
         if dst is None:
-            dst = (_empty((B, N, H, 128), t, dev, stream) if inverse else
-                   _empty((B, H, N, 128), t, dev, stream).transpose(1, 2))
-        sides.append((H, vin, _view4(dst, f"rotary: {name}_out", B, N, H, t, dev), dst))
+            dst = _empty(shape, t, dev, stream, None if inverse else (H * N * 128, 128, N * 128, 1))
+        sides.append((H, vin, _view4(dst, name + "_out", shape, t, dev), dst))
     pos = _plain(positions, "rotary: positions", (r.naxes, B, N), torch.int32, dev)
     (Hq, qi, qo, qd), (Hkv, ki, ko, kd) = sides
     _call_on(dev, stream, lib().s2o_rotary, "s2o_rotary", r, FP16 if t is torch.float16 else BF16, B, N, Hq, Hkv, qi,
@@ -448,14 +459,16 @@ def cache_append(cfg: CacheConfig, q, k, v, k_cache, v_cache, page_table, q_star
     dev, t, T = k.device, _torch_type(cfg.dtype), cfg.Tq
     qv = qo = None
     if q is not None:
-        qv = _view3(q, "cache_append: q", cfg.Hq, T, t, dev)
+        shape = (T, cfg.Hq, 128)
+        qv = _view3(q, "cache_append: q", shape, t, dev)
         if q_out is None:
-            q_out = _empty((T, cfg.Hq, 128), t, dev, stream)
-        qo = _view3(q_out, "cache_append: q_out", cfg.Hq, T, t, dev)
+            q_out = _empty(shape, t, dev, stream)
+        qo = _view3(q_out, "cache_append: q_out", shape, t, dev)
     elif q_out is not None:
         _refuse("cache_append: q_out without q")
-    kv = _view3(k, "cache_append: k", cfg.Hkv, T, t, dev)
-    vv = _view3(v, "cache_append: v", cfg.Hkv, T, t, dev)
+    shape = (T, cfg.Hkv, 128)
+    kv = _view3(k, "cache_append: k", shape, t, dev)
+    vv = _view3(v, "cache_append: v", shape, t, dev)
     kc, vc, table, qs, kl = _cache_args(cfg, k_cache, v_cache, page_table, q_start, kv_len, dev, t)
     pos = None
     if positions is not None:

@@ -93,7 +93,7 @@ PagedPlan paged_plan(const s2o_cache_config* c) {
 
 struct PagedWs {
   int64_t* units;   // of the tile kernel, of the decode kernel
-  int2* meta;
+  int4* meta;
   SplitItem* split;
   PagedPart tile, decode;
   size_t bytes;
@@ -112,7 +112,7 @@ PagedWs paged_layout(const s2o_cache_config* c, const PagedPlan& p, int n, void*
   if (c->prefix_len == 0 || p.chunks) {  // whole items are the result
     w.split = static_cast<SplitItem*>(take((size_t)(p.chunks ? n : streams) * sizeof(SplitItem)));
   } else {
-    w.meta = static_cast<int2*>(take((size_t)c->Tq * c->Hkv * sizeof(int2)));
+    w.meta = static_cast<int4*>(take((size_t)c->Tq * c->Hkv * sizeof(int4)));
     for (int k = 0; k < 2; ++k) {
       w.decode.dense[k] = static_cast<float*>(take(rows * kD * sizeof(float)));
       w.decode.dense_ml[k] = static_cast<float2*>(take(rows * sizeof(float2)));
@@ -144,6 +144,23 @@ bool encode_query_map(CUtensorMap* map, const void* base, int Tq, int Hq, int G,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// launch that may start before the kernel in front of it is done
+template <class... P, class... A>
+cudaError_t launch_early(void (*f)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s, bool early,
+                         const A&... args) {
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, f, args...);
+}
+
 template <bool FP16>
 cudaError_t launch_tile(const PagedArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, int n,
                         cudaStream_t s) {
@@ -154,20 +171,20 @@ cudaError_t launch_tile(const PagedArgs& a, const CUtensorMap& q, const CUtensor
   return cudaGetLastError();
 }
 template <bool FP16, int R>
-cudaError_t launch_decode(const PagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, int n, cudaStream_t s) {
+cudaError_t launch_decode(const PagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, int n, cudaStream_t s,
+                          bool early) {
   // the attribute belongs to the function on the current device; setting it
   // again costs less than a microsecond
   cudaError_t e = cudaFuncSetAttribute(k_paged_decode<FP16, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)PgDecode<R>::kSmem);
   if (e != cudaSuccess) return e;
-  k_paged_decode<FP16, R><<<n, 32 * kPgWarps, PgDecode<R>::kSmem, s>>>(a, k, v);
-  return cudaGetLastError();
+  return launch_early(k_paged_decode<FP16, R>, n, 32 * kPgWarps, PgDecode<R>::kSmem, s, early, a, k, v);
 }
 template <bool FP16>
 cudaError_t launch_decode_r(int R, const PagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, int n,
-                            cudaStream_t s) {
-  return R == 1 ? launch_decode<FP16, 1>(a, k, v, n, s)
-                : (R == 2 ? launch_decode<FP16, 2>(a, k, v, n, s) : launch_decode<FP16, 4>(a, k, v, n, s));
+                            cudaStream_t s, bool early) {
+  return R == 1 ? launch_decode<FP16, 1>(a, k, v, n, s, early)
+                : (R == 2 ? launch_decode<FP16, 2>(a, k, v, n, s, early) : launch_decode<FP16, 4>(a, k, v, n, s, early));
 }
 
 }  // namespace
@@ -293,8 +310,9 @@ s2o_status s2o_attention_paged(const s2o_cache_config* cfg, const uint16_t* Q, c
     a.c = p.decode;
     a.part = w.decode;
     a.units = w.units + 1;
-    if ((fp16 ? launch_decode_r<true>(p.R, a, tmK, tmV, n, s) : launch_decode_r<false>(p.R, a, tmK, tmV, n, s)) !=
-        cudaSuccess)
+    // beside the tile kernel: neither reads what the other writes
+    if ((fp16 ? launch_decode_r<true>(p.R, a, tmK, tmV, n, s, p.tiles)
+              : launch_decode_r<false>(p.R, a, tmK, tmV, n, s, p.tiles)) != cudaSuccess)
       return S2O_ERR_CUDA;
     ++t_launches;
   }
@@ -305,15 +323,15 @@ s2o_status s2o_attention_paged(const s2o_cache_config* cfg, const uint16_t* Q, c
   j.prefix = p.tiles ? tile : decode;
   j.own = p.chunks ? tile : decode;
   j.meta = w.meta; j.split = w.split; j.O = O; j.lse = lse; j.out_f32 = a.out_f32;
+  cudaError_t e;
   if (a.direct) {
     const dim3 grid(j.own.n, (j.own.part.rows + 31) / 32);
-    if (fp16) k_paged_join_split<true><<<grid, 256, 0, s>>>(j);
-    else k_paged_join_split<false><<<grid, 256, 0, s>>>(j);
+    e = launch_early(fp16 ? k_paged_join_split<true> : k_paged_join_split<false>, grid, 256, 0, s, true, j);
   } else {
     const unsigned blocks = (unsigned)(((int64_t)cfg->Tq * cfg->Hq + 7) / 8);
-    if (fp16) k_paged_join<true><<<blocks, 256, 0, s>>>(j);
-    else k_paged_join<false><<<blocks, 256, 0, s>>>(j);
+    e = launch_early(fp16 ? k_paged_join<true> : k_paged_join<false>, blocks, 256, 0, s, true, j);
   }
+  if (e != cudaSuccess) return S2O_ERR_CUDA;
   ++t_launches;
   return launch_status();
 }

@@ -77,7 +77,7 @@ struct PagedArgs {
   void* O;
   float* lse;         // [Tq, Hq] or null
   PagedPart part;
-  int2* meta;         // [Tq, Hkv]: first and last share of the own item a token's rows are in (join of rows)
+  int4* meta;         // [Tq, Hkv]: first and last share of the token's own item, its place in the tile (join of rows)
   SplitItem* split;   // [workers] (join of split items)
   int64_t* units;     // total units of this kernel, for the join
   int out_f32;
@@ -118,6 +118,11 @@ __device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* m
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
+// Programmatic launch: the kernel behind this one may start on SMs that this
+// one leaves; and the wait until the kernel in front is done and its writes
+// are seen (both nothing when the launch did not ask for it).
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 // two neighbouring values of a finished row
 template <bool FP16>
 __device__ __forceinline__ void store2(void* O, int out_f32, size_t at, float x, float y) {
@@ -147,7 +152,7 @@ __device__ __forceinline__ void announce_split(const PagedArgs& a, const Sched& 
     const int me = sc.me;
     const int c1 = p.last ? me : split_end(sc);
     if (!a.direct) {
-      for (int t = lane; t < p.ntok; t += 32) a.meta[(int64_t)(p.tok0 + t) * a.g.Hkv + p.kvh] = make_int2(me, c1);
+      for (int t = lane; t < p.ntok; t += 32) a.meta[(int64_t)(p.tok0 + t) * a.g.Hkv + p.kvh] = make_int4(me, c1, t, 0);
     } else if (!p.last) {
       split = {p.tok0, p.ntok, p.kvh, c1};
     }
@@ -174,6 +179,7 @@ __global__ void __launch_bounds__(32 * kPgWarps, 1)
   };
   static_assert(sizeof(Piece) <= 64, "piece slot");
   const PagedGeom& g = a.g;
+  let_next_start();
 
   if (rt == 0 && lane < C::kStages) {
     mbar_init(full(lane), 1);
@@ -416,6 +422,9 @@ __global__ void __launch_bounds__(32 * kPgWarps, 1)
       if (!mbar_wait_bounded(full(k % C::kStages), (k / C::kStages) & 1)) {
         if (lane == 0) set_error(kErrTimeout);
       }
+  // nothing here reads what the kernel in front wrote, but the join, which
+  // waits for this one alone, does
+  wait_for_previous();
 }
 
 // ---------------------------------------------------------------------------
@@ -436,7 +445,7 @@ struct JoinSide {
 struct JoinArgs {
   PagedGeom g;
   JoinSide prefix, own;
-  const int2* meta;
+  const int4* meta;
   const SplitItem* split;
   void* O;
   float* lse;
@@ -457,14 +466,14 @@ __device__ __forceinline__ float warp_add(float x) {
   for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
-// cnt parts; lane l of a batch of 32 has part l's (reference, sum) from
-// ml_of(j, row of the accumulators); a part that saw no key has (-inf, 0)
+// cnt parts; lane l of a batch of 32 gets part l's (reference, sum) and
+// accumulators from part(j, acc); one that saw no key has (-inf, 0)
 template <class F>
-__device__ __forceinline__ void add_parts(RowSum& s, const float* acc, int cnt, int lane, F ml_of) {
+__device__ __forceinline__ void add_parts(RowSum& s, int cnt, int lane, F part) {
   for (int base = 0; base < cnt; base += 32) {
-    size_t at = 0;
+    const float* acc = nullptr;
     float2 ml = make_float2(-INFINITY, 0.f);
-    if (base + lane < cnt) ml = ml_of(base + lane, at);
+    if (base + lane < cnt) ml = part(base + lane, acc);
     const float m = fmaxf(s.m, warp_max(ml.x));
     const float w = ml.x == -INFINITY && ml.y == 0.f ? 0.f : ex2_approx(ml.x - m);
     const float f = s.m == -INFINITY ? 0.f : ex2_approx(s.m - m);
@@ -472,29 +481,34 @@ __device__ __forceinline__ void add_parts(RowSum& s, const float* acc, int cnt, 
     s.l = s.l * f + warp_add(ml.y * w);
     s.o = make_float4(s.o.x * f, s.o.y * f, s.o.z * f, s.o.w * f);
     const int n = min(32, cnt - base);
-#pragma unroll 8
-    for (int k = 0; k < n; ++k) {
-      const float wk = __shfl_sync(0xffffffffu, w, k);
-      const size_t ak = __shfl_sync(0xffffffffu, at, k);
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (wk != 0.f) v = reinterpret_cast<const float4*>(acc + ak * kD)[lane];
-      s.o = make_float4(fmaf(v.x, wk, s.o.x), fmaf(v.y, wk, s.o.y), fmaf(v.z, wk, s.o.z), fmaf(v.w, wk, s.o.w));
+    for (int k0 = 0; k0 < n; k0 += 8) {
+      float4 v[8];
+      float wk[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        wk[k] = __shfl_sync(0xffffffffu, w, k0 + k);
+        const float4* a = reinterpret_cast<const float4*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(acc), k0 + k));
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (wk[k] != 0.f) v[k] = a[lane];  // lanes behind the last part have weight 0
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        s.o = make_float4(fmaf(v[k].x, wk[k], s.o.x), fmaf(v[k].y, wk[k], s.o.y), fmaf(v[k].z, wk[k], s.o.z),
+                          fmaf(v[k].w, wk[k], s.o.w));
     }
   }
 }
-// parts of shares c0 .. c1; member `offset` of teams of `stride`
-__device__ __forceinline__ void add_split(RowSum& s, const PagedPart& part, int c0, int c1, int stride, int offset,
-                                          int tile_row, int lane) {
-  add_parts(s, part.slots, c1 - c0 + 1, lane, [&](int j, size_t& at) {
-    at = (size_t)(2 * ((c0 + j) * stride + offset) + (j == 0 ? 1 : 0)) * part.rows + tile_row;
-    return part.slots_ml[at];
-  });
+// part j of an item in shares c0 .. (member `offset` of teams of `stride`)
+__device__ __forceinline__ float2 split_part(const PagedPart& part, int c0, int j, int stride, int offset,
+                                             int tile_row, const float*& acc) {
+  const size_t at = (size_t)(2 * ((c0 + j) * stride + offset) + (j == 0 ? 1 : 0)) * part.rows + tile_row;
+  acc = part.slots + at * kD;
+  return part.slots_ml[at];
 }
-__device__ __forceinline__ void add_dense(RowSum& s, const PagedPart& part, int kind, size_t row, int lane) {
-  add_parts(s, part.dense[kind], 1, lane, [&](int, size_t& at) {
-    at = row;
-    return part.dense_ml[kind][row];
-  });
+__device__ __forceinline__ float2 dense_part(const PagedPart& part, int kind, size_t row, const float*& acc) {
+  acc = part.dense[kind] + row * kD;
+  return part.dense_ml[kind][row];
 }
 template <bool FP16>
 __device__ __forceinline__ void finish_row(const JoinArgs& a, const RowSum& s, size_t row, int lane) {
@@ -515,32 +529,31 @@ __global__ void __launch_bounds__(256) k_paged_join(const __grid_constant__ Join
   const int lane = threadIdx.x & 31;
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
   const int t = row / g.Hq, h = row - t * g.Hq;
+  wait_for_previous();
   if (t >= g.Tq) return;
   const int ntok = batch_tokens(g);
   const int kvh = h / g.G, hh = h - kvh * g.G;
-  int2 own = a.meta[(int64_t)t * g.Hkv + kvh];
+  int4 own = a.meta[(int64_t)t * g.Hkv + kvh];
   const int64_t PU = *a.prefix.units;
   if (t >= ntok) return;
   own.x = max(0, min(own.x, a.own.n - 1));  // rows of a refused sequence were never written
   own.y = max(own.x, min(own.y, a.own.n - 1));
+  own.z = max(0, min(own.z, a.own.c.tpt - 1));
+  const PagedCut& c = a.prefix.c;
+  const int npt = (ntok + c.tpt - 1) / c.tpt, rt = t / c.tpt;
+  const int64_t np = ((int64_t)g.prefix + (1 << c.kt_log2) - 1) >> c.kt_log2;
+  const int team = team_size(c, npt, a.prefix.n), n = shares_of(PU, a.prefix.n / team);
+  const int64_t u0 = (team > 1 ? (int64_t)kvh : (int64_t)kvh * npt + rt) * np;
+  const int c0 = share_owner(PU, n, u0), c1 = share_owner(PU, n, u0 + np - 1);
+  const int parts = c1 - c0 + 1, member = team > 1 ? rt : 0, prow = (t - rt * c.tpt) * g.G + hh;
   RowSum s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-  {
-    const PagedCut& c = a.prefix.c;
-    const int npt = (ntok + c.tpt - 1) / c.tpt, rt = t / c.tpt;
-    const int64_t np = ((int64_t)g.prefix + (1 << c.kt_log2) - 1) >> c.kt_log2;
-    const int team = team_size(c, npt, a.prefix.n), n = shares_of(PU, a.prefix.n / team);
-    const int64_t u0 = (team > 1 ? (int64_t)kvh : (int64_t)kvh * npt + rt) * np;
-    const int c0 = share_owner(PU, n, u0), c1 = share_owner(PU, n, u0 + np - 1);
-    if (c0 == c1) add_dense(s, a.prefix.part, 0, row, lane);
-    else add_split(s, a.prefix.part, c0, c1, team, team > 1 ? rt : 0, (t - rt * c.tpt) * g.G + hh, lane);
-  }
-  if (own.x == own.y) {
-    add_dense(s, a.own.part, 1, row, lane);
-  } else {  // the token's place in its row tile
-    const int q0 = g.q_start[seq_of_token(g.q_start, g.nseq, t)];
-    const int tr = max(0, (t - q0) % a.own.c.tpt) * g.G + hh;
-    add_split(s, a.own.part, own.x, own.y, 1, 0, tr, lane);
-  }
+  add_parts(s, parts + own.y - own.x + 1, lane, [&](int j, const float*& acc) {
+    if (j < parts)
+      return parts == 1 ? dense_part(a.prefix.part, 0, row, acc)
+                        : split_part(a.prefix.part, c0, j, team, member, prow, acc);
+    return own.x == own.y ? dense_part(a.own.part, 1, row, acc)
+                          : split_part(a.own.part, own.x, j - parts, 1, 0, own.z * g.G + hh, acc);
+  });
   finish_row<FP16>(a, s, row, lane);
 }
 
@@ -549,12 +562,14 @@ __global__ void __launch_bounds__(256) k_paged_join(const __grid_constant__ Join
 template <bool FP16>
 __global__ void __launch_bounds__(256) k_paged_join_split(const __grid_constant__ JoinArgs a) {
   const PagedGeom& g = a.g;
+  wait_for_previous();
   const SplitItem it = a.split[blockIdx.x];
   const int lane = threadIdx.x & 31;
   for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < it.ntok * g.G; r += gridDim.y * 8) {
     const int t = r / g.G;
     RowSum s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    add_split(s, a.own.part, blockIdx.x, it.c1, 1, 0, r, lane);
+    add_parts(s, it.c1 - (int)blockIdx.x + 1, lane,
+              [&](int j, const float*& acc) { return split_part(a.own.part, blockIdx.x, j, 1, 0, r, acc); });
     finish_row<FP16>(a, s, (size_t)(it.tok0 + t) * g.Hq + it.kvh * g.G + (r - t * g.G), lane);
   }
 }

@@ -74,6 +74,15 @@ __device__ __forceinline__ TileKeys tile_keys(const PagedGeom& g, const Piece& p
   return k;
 }
 
+// eight floats, one 32-byte store: a thread writes its own row, so a warp's
+// store touches 32 lines whatever its width, and half as many stores take
+// half the time
+__device__ __forceinline__ void store_sector(float* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
 template <bool FP16>
 __global__ void __launch_bounds__(kAttn2Threads, 1)
     k_paged_tile(const __grid_constant__ PagedArgs a, const __grid_constant__ CUtensorMap tmQ,
@@ -89,6 +98,7 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
   const int tpt = kLq / g.G;      // tokens of a 128-row tile
   const int trows = tpt * g.G;    // its rows
 
+  let_next_start();
   if (tid == 0) {
     for (int k = 0; k < kPtBars; ++k) {
       uint32_t count = 1;
@@ -439,9 +449,8 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
         tc_wait_ld();
         if (!has) {
         } else if (!final) {
-          float4* dst = reinterpret_cast<float4*>(part + cc);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          for (int k = 0; k < 4; ++k) store_sector(part + cc + 8 * k, o + 8 * k);
         } else if (a.out_f32) {
           float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.O) + orow * kD + cc);
 #pragma unroll
