@@ -346,9 +346,13 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
       const int rows = rows_of(p, qi);
       if (rows == 0) continue;
       const bool has = r < rows;
-      // keys the row sees: of the prefix all, of its own up to itself
-      const int see_own = has ? p.off + qi * tpt + rt + 1 : 0;
-      const int see_pre = has ? g.prefix : 0;
+      // keys the row sees: of the prefix all, of its own up to itself.  Rows of
+      // nobody see what the last row sees: were they masked, their warp would
+      // go through both forms of the exponentials below (one such warp in a CTA
+      // made its tiles 20 % slower); a warp of them alone does nothing
+      const int see_own = p.off + qi * tpt + min(rt, rows / g.G - 1) + 1;
+      const int see_pre = g.prefix;
+      const bool idle = (tid & 96) >= rows;
       float m_run = -INFINITY, ell = 0.f;
       const int nch = 2 * (p.tile1 - p.tile0);
       for (int c = 0; ok && c < nch; ++c) {
@@ -358,6 +362,15 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
         const int vis = (pre ? see_pre - t * kPtKeys : see_own - (t - p.np) * kPtKeys) - kBk * (c & 1);
         if (!warp_wait(bar(kBarSFull + qi), n & 1, kSpinLimit)) { ok = false; break; }
         tc_fence_after();
+        if (idle) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(kBarSEmpty + qi));
+            mbar_arrive(bar(kBarPFull + 2 * qi + (c & 1)));
+          }
+          continue;
+        }
         float x[kBk];
         tmem_ld32(tS, x);
         tmem_ld32(tS + 32, x + 32);
