@@ -54,6 +54,31 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// Shared-memory descriptors of 128-byte swizzled tiles as two words: the high
+// one is the same for all (8-row groups 1024 bytes apart, version 1, swizzle),
+// the low one holds address / 16, to which offsets / 16 are added, and the
+// leading dimension's offset (see sdesc_sw128).
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
+  return ((saddr >> 4) & 0x3FFFu) | ((lbo_bytes >> 4) << 16);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n"
+      " setp.ne.b32 p, %4, 0;\n mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(add), "r"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 b;\n"
+      " setp.ne.b32 p, %4, 0;\n mov.b64 b, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(add), "r"(kDescHi)
+      : "memory");
+}
+
 // tile t of a piece: its page list, first key in it, and the keys the piece's
 // rows can reach there
 struct TileKeys {
@@ -227,10 +252,17 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
       const uint32_t idesc_qk = (idesc_bf16_f32(128, kBk, false) & ~((7u << 7) | (7u << 10))) | kTypes;
       const uint32_t idesc_pv = (idesc_bf16_f32(128, 128, true) & ~((7u << 7) | (7u << 10))) | kTypes;
       bool ok = true;
-      uint32_t kt = 0;  // tiles so far (K and V rings)
-      uint32_t gc = 0;  // chunks of this head so far
+      uint32_t ks = 0, kph = 0, vs = 0, vph = 0;  // ring stages and their parities
+      uint32_t gt = 0;  // tiles of this head so far
       uint32_t np = 0;  // pieces this head had rows in
       uint32_t nq = 0;  // Q tiles asked for
+      const uint32_t tS = tmem + col_s(i), tO = tmem + col_o(i), tP = tmem + col_p(i, 0);
+      const uint32_t lo_q = desc_lo(sbase + kOff2Q + i * kTile2Bytes, 16);
+      const uint32_t lo_k = desc_lo(sbase + kOff2K, 16), lo_v = desc_lo(sbase + kOff2V, 128 * 128);
+      auto wait = [&](int slot, uint32_t parity) {
+        ok = ok && mbar_wait_bounded(bar(slot), parity);
+        return ok;
+      };
       auto fetch_q = [&](const Piece& p) {
         if (p.kind < 0 || rows_of(p, i) == 0) return;
         mbar_expect_tx(bar(kPtQFull + i), (uint32_t)trows * 256);
@@ -239,6 +271,28 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
                       bar(kPtQFull + i));
         ++nq;
       };
+      // S of half h of the K stage: 8 products of 16 columns
+      auto qk = [&](int h) {
+        tc_fence_after();
+        const uint32_t k0 = lo_k + ks * (kTile2Bytes >> 4) + h * (kBk * 128 >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t at = (kk >> 2) * (128 * 128 >> 4) + (kk & 3) * 2;
+          mma_ss(tS, lo_q + at, k0 + at, idesc_qk, kk > 0 ? 1u : 0u);
+        }
+        tc_commit(bar(kBarSFull + i));
+      };
+      // O (+)= P of half h times that half of the V stage: 4 products of 16 keys
+      auto pv = [&](int h, bool add) {
+        tc_fence_after();
+        const uint32_t v0 = lo_v + vs * (kTile2Bytes >> 4) + h * (kBk * 128 >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kBk / 16; ++kk)
+          mma_ts(tO, tP + 32 * h + 8 * kk, v0 + kk * (16 * 128 >> 4), idesc_pv, add || kk > 0 ? 1u : 0u);
+        tc_commit(bar(kBarODone + 2 * i + h));
+      };
+      auto leave_k = [&]() { if (++ks == kStagesK) { ks = 0; kph ^= 1; } };
+      auto leave_v = [&]() { if (++vs == kStagesV) { vs = 0; vph ^= 1; } };
       Piece p, next;
       ok = take_piece(0, next);
       if (ok) fetch_q(next);
@@ -246,78 +300,53 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
         p = next;
         mbar_arrive(bar(kPtPieceEmpty + pi % kPieceSlots));
         if (p.kind < 0) break;
-        const int ntiles = p.tile1 - p.tile0, nch = 2 * ntiles;
+        const int ntiles = p.tile1 - p.tile0;
         if (rows_of(p, i) == 0) {  // let the stages pass
           for (int t = 0; ok && t < ntiles; ++t) {
-            const uint32_t k = kt + t;
-            ok = mbar_wait_bounded(bar(kBarKFull + k % kStagesK), (k / kStagesK) & 1);
-            if (ok) mbar_arrive(bar(kBarKEmpty + k % kStagesK));
-            if (ok) ok = mbar_wait_bounded(bar(kBarVFull + k % kStagesV), (k / kStagesV) & 1);
-            if (ok) mbar_arrive(bar(kBarVEmpty + k % kStagesV));
+            if (!wait(kBarKFull + ks, kph)) break;
+            mbar_arrive(bar(kBarKEmpty + ks));
+            leave_k();
+            if (!wait(kBarVFull + vs, vph)) break;
+            mbar_arrive(bar(kBarVEmpty + vs));
+            leave_v();
           }
-          kt += ntiles;
           if (ok) ok = take_piece(pi + 1, next);
           if (ok) fetch_q(next);
           continue;
         }
-        ok = mbar_wait_bounded(bar(kPtQFull + i), np & 1);
-        for (int c = 0; ok && c <= nch; ++c) {
-          if (c < nch) {
-            const int h = c & 1;
-            const uint32_t k = kt + (c >> 1);
-            if (h == 0) {
-              ok = mbar_wait_bounded(bar(kBarKFull + k % kStagesK), (k / kStagesK) & 1);
-              if (!ok) break;
-            }
-            const uint32_t n = gc + c;
-            if (n > 0) {
-              ok = mbar_wait_bounded(bar(kBarSEmpty + i), (n - 1) & 1);
-              if (!ok) break;
-            }
-            tc_fence_after();
-            const uint32_t sQ = sbase + kOff2Q + i * kTile2Bytes;
-            const uint32_t sK = sbase + kOff2K + (k % kStagesK) * kTile2Bytes + kBk * h * 128;
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              const uint64_t ad = sdesc_sw128(sQ + (kk >> 2) * (128 * 128) + (kk & 3) * 32, 16, 1024);
-              const uint64_t bd = sdesc_sw128(sK + (kk >> 2) * (128 * 128) + (kk & 3) * 32, 16, 1024);
-              tc_mma_ss(tmem + col_s(i), ad, bd, idesc_qk, kk > 0 ? 1u : 0u);
-            }
-            tc_commit(bar(kBarSFull + i));
-            if (h == 1) tc_commit(bar(kBarKEmpty + k % kStagesK));
+        // chunk by chunk (half tiles): S of a chunk as soon as the softmax has
+        // read S of the one before, then P V of the one before.  The thread
+        // does little but issue: descriptors are a base plus constants, stages
+        // and parities are counted, since its instructions, one warp's chain,
+        // are what the tensor core waits for.
+        if (!wait(kPtQFull + i, np & 1)) break;
+        for (int t = 0; t < ntiles; ++t, ++gt) {
+          if (!wait(kBarKFull + ks, kph)) break;
+          if (gt > 0 && !wait(kBarSEmpty + i, 1)) break;
+          qk(0);
+          if (t > 0) {
+            if (!wait(kBarPFull + 2 * i + 1, (gt - 1) & 1)) break;
+            pv(1, true);
+            tc_commit(bar(kBarVEmpty + vs));
+            leave_v();
           }
-          if (c > 0) {
-            const int cp = c - 1, hp = cp & 1;
-            const uint32_t k = kt + (cp >> 1), n = gc + cp;
-            if (hp == 0) {
-              ok = mbar_wait_bounded(bar(kBarVFull + k % kStagesV), (k / kStagesV) & 1);
-              if (!ok) break;
-            }
-            ok = mbar_wait_bounded(bar(kBarPFull + 2 * i + hp), (n >> 1) & 1);
-            if (!ok) break;
-            // the accumulator of the piece before this one has been read
-            if (cp == 0 && np > 0) {
-              ok = mbar_wait_bounded(bar(kPtOFree + i), (np - 1) & 1);
-              if (!ok) break;
-            }
-            if (cp == nch - 1) {  // the softmax took the last scores: Q is free
-              ok = take_piece(pi + 1, next);
-              if (!ok) break;
-              fetch_q(next);
-            }
-            tc_fence_after();
-            const uint32_t sV = sbase + kOff2V + (k % kStagesV) * kTile2Bytes;
-#pragma unroll
-            for (int kk = 0; kk < kBk / 16; ++kk) {
-              const uint64_t bd = sdesc_sw128(sV + (kBk * hp + 16 * kk) * 128, 128 * 128, 1024);
-              tc_mma_ts(tmem + col_o(i), tmem + col_p(i, hp) + 8 * kk, bd, idesc_pv, (cp > 0 || kk > 0) ? 1u : 0u);
-            }
-            tc_commit(bar(kBarODone + 2 * i + hp));
-            if (hp == 1) tc_commit(bar(kBarVEmpty + k % kStagesV));
-          }
+          if (!wait(kBarSEmpty + i, 0)) break;
+          qk(1);
+          tc_commit(bar(kBarKEmpty + ks));
+          leave_k();
+          if (!wait(kBarVFull + vs, vph) || !wait(kBarPFull + 2 * i, gt & 1)) break;
+          // the accumulator of the piece before this one has been read
+          if (t == 0 && np > 0 && !wait(kPtOFree + i, (np - 1) & 1)) break;
+          pv(0, t > 0);
         }
-        kt += ntiles;
-        gc += nch;
+        if (!ok || !wait(kBarPFull + 2 * i + 1, (gt - 1) & 1)) break;
+        // the softmax took the last scores: Q is free for the next piece
+        ok = take_piece(pi + 1, next);
+        if (!ok) break;
+        fetch_q(next);
+        pv(1, true);
+        tc_commit(bar(kBarVEmpty + vs));
+        leave_v();
         ++np;
       }
       if (!ok) set_error(kErrTimeout);
@@ -329,6 +358,12 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
     // ------------------------------------------------------------------ softmax
     regs_increase<kRegsSoftmax>();
     constexpr float kShift = FP16 ? 7.f : 0.f;
+    // A row's reference is the maximum of the first keys it saw.  Later ones
+    // need no maximum: numbers with an exponent lose nothing by being large,
+    // so the reference moves only when a chunk's sum says that P may leave its
+    // type's range (fp16: 2^15; bf16: far from fp32's end, which O and the sum
+    // must keep clear of)
+    constexpr float kPtMove = FP16 ? 32768.f : 1.15e18f;
     const int qi = warp >> 2;
     const int r = tid & 127;
     const int rt = r / g.G, rh = r - rt * g.G;  // token of the tile, head of the group
@@ -379,64 +414,70 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarSEmpty + qi));
         const bool full = vis >= kBk;
-        float mt = -INFINITY;
-        if (full) {
+        // the largest score the row sees in this chunk, as a reference
+        auto reference = [&]() {
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int k = 0; k < kBk; k += 2) m4[(k >> 1) & 3] = fmax3(m4[(k >> 1) & 3], x[k], x[k + 1]);
-          mt = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
-        } else {
+          for (int k = 0; k < kBk; ++k) m4[k & 3] = fmaxf(m4[k & 3], full || k < vis ? x[k] : -INFINITY);
+          return fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), kPgScale, -kShift);
+        };
+        float pw[kBk / 2], rs;  // P as pairs, their sum
+        auto exponentials = [&]() {
+          if (full) {
+            const uint64_t s2 = f2_pack(kPgScale, kPgScale), nm2 = f2_pack(-m_run, -m_run);
+            uint64_t rs2 = 0;
 #pragma unroll
-          for (int k = 0; k < kBk; ++k)
-            if (k < vis) mt = fmaxf(mt, x[k]);
+            for (int k = 0; k < kBk; k += 2) {
+              const uint64_t v = f2_fma(f2_pack(x[k], x[k + 1]), s2, nm2);
+              const float p0 = ex2_approx(f2_lo(v)), p1 = ex2_approx(f2_hi(v));
+              rs2 = f2_add(rs2, f2_pack(p0, p1));
+              pw[k / 2] = __uint_as_float(pack2<FP16>(p0, p1));
+            }
+            rs = f2_lo(rs2) + f2_hi(rs2);
+          } else {
+            rs = 0.f;
+#pragma unroll
+            for (int k = 0; k < kBk; k += 2) {
+              const float p0 = (k < vis) ? ex2_approx(fmaf(x[k], kPgScale, -m_run)) : 0.f;
+              const float p1 = (k + 1 < vis) ? ex2_approx(fmaf(x[k + 1], kPgScale, -m_run)) : 0.f;
+              rs += p0 + p1;
+              pw[k / 2] = __uint_as_float(pack2<FP16>(p0, p1));
+            }
+          }
+        };
+        // the first keys a row sees set its reference (nothing to rescale: its
+        // accumulator and sum are zero)
+        if (__any_sync(0xffffffffu, m_run == -INFINITY)) {
+          const float mt = reference();
+          if (m_run == -INFINITY) m_run = mt;
         }
-        mt = fmaf(mt, kPgScale, -kShift);
-        const bool move = mt > m_run + 8.f;
-        float alpha = 1.f;
-        if (move) {
-          alpha = (m_run == -INFINITY) ? 0.f : ex2_approx(m_run - mt);
-          m_run = mt;
+        exponentials();
+        if (__any_sync(0xffffffffu, rs > kPtMove)) {
+          const float mt = reference();
+          const bool move = rs > kPtMove;
+          const float alpha = move ? ex2_approx(m_run - mt) : 1.f;
+          if (move) m_run = mt;
           ell *= alpha;
+          if (c > 0) {
+            if (!warp_wait(bar(kBarODone + 2 * qi + ((n - 1) & 1)), ((n - 1) >> 1) & 1, kSpinLimit)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int cc = 0; cc < 128; cc += 32) {
+              float o[32];
+              tmem_ld32(tO + cc, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] *= alpha;
+              tmem_st32(tO + cc, o);
+            }
+          }
+          exponentials();
         }
-        if (c > 0 && __any_sync(0xffffffffu, move)) {
-          if (!warp_wait(bar(kBarODone + 2 * qi + ((n - 1) & 1)), ((n - 1) >> 1) & 1, kSpinLimit)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-#pragma unroll
-          for (int cc = 0; cc < 128; cc += 32) {
-            float o[32];
-            tmem_ld32(tO + cc, o);
-            tc_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] *= alpha;
-            tmem_st32(tO + cc, o);
-          }
-        }
-        if (full) {
-          const uint64_t s2 = f2_pack(kPgScale, kPgScale), nm2 = f2_pack(-m_run, -m_run);
-          uint64_t rs2 = 0;
-#pragma unroll
-          for (int k = 0; k < kBk; k += 2) {
-            const uint64_t v = f2_fma(f2_pack(x[k], x[k + 1]), s2, nm2);
-            const float p0 = ex2_approx(f2_lo(v)), p1 = ex2_approx(f2_hi(v));
-            rs2 = f2_add(rs2, f2_pack(p0, p1));
-            x[k / 2] = __uint_as_float(pack2<FP16>(p0, p1));
-          }
-          ell += f2_lo(rs2) + f2_hi(rs2);
-        } else {
-          float rs = 0.f;
-#pragma unroll
-          for (int k = 0; k < kBk; k += 2) {
-            const float p0 = (k < vis) ? ex2_approx(fmaf(x[k], kPgScale, -m_run)) : 0.f;
-            const float p1 = (k + 1 < vis) ? ex2_approx(fmaf(x[k + 1], kPgScale, -m_run)) : 0.f;
-            rs += p0 + p1;
-            x[k / 2] = __uint_as_float(pack2<FP16>(p0, p1));
-          }
-          ell += rs;
-        }
-        tmem_st32(tmem + col_p(qi, c & 1) + lane_base, x);
+        ell += rs;
+        tmem_st32(tmem + col_p(qi, c & 1) + lane_base, pw);
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
