@@ -8,6 +8,11 @@
 // tcgen05 tiles of 128 (G query heads of 128 / G tokens each), that share
 // every K/V tile; roles, tensor-memory layout, chunked softmax and register
 // split are those of k_sparse_attn2 (see there), with these differences:
+//   * S is double buffered, P written over the scores it came from (O and S fill
+//     the 512 columns), so that the products of the next half tile run during
+//     the softmax of this one; with one buffer a head the tensor core, the
+//     softmax and their hand-overs follow one another (1840 clocks a half tile
+//     of both heads, of which the products are about 1280);
 //   * keys come from pages: warps 9 and 10 issue TMA boxes (64 columns x
 //     min(page, 64) rows, 128-byte swizzle) into the K and V rings; the last
 //     tile of a list that ends inside it has its missing V rows zeroed in
@@ -37,6 +42,7 @@ constexpr size_t kPtSmem = kPtSmemData + 1024;
 static_assert(kPtSmem <= 227 * 1024, "shared memory");
 
 // barrier slots; those of k_sparse_attn2 up to the P and O ones
+constexpr int kPtSFull = kBarSFull;  // [2][2] MMA commit (S_i,b written) -> softmax i; slot + 2 i + b
 constexpr int kPtOFree = 23;       // [2] softmax i, one arrive per warp: O_i was read -> issuer i
 constexpr int kPtVTmp = 25;        // V loader's own: boxes of a ragged tile landed
 constexpr int kPtDrain = 26;       // [2]
@@ -53,6 +59,10 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
+
+// two score buffers of 64 keys a head; P (32 columns) takes the place of the
+// scores it was made from
+__device__ __forceinline__ uint32_t col_sp(int i, int b) { return 256u + 128u * i + 64u * b; }
 
 // Shared-memory descriptors of 128-byte swizzled tiles as two words: the high
 // one is the same for all (8-row groups 1024 bytes apart, version 1, swizzle),
@@ -127,9 +137,7 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
   if (tid == 0) {
     for (int k = 0; k < kPtBars; ++k) {
       uint32_t count = 1;
-      if ((k >= kBarSEmpty && k < kBarSEmpty + 2) || (k >= kBarPFull && k < kBarPFull + 4) ||
-          (k >= kPtOFree && k < kPtOFree + 2))
-        count = 4;
+      if ((k >= kBarPFull && k < kBarPFull + 4) || (k >= kPtOFree && k < kPtOFree + 2)) count = 4;
       if ((k >= kBarKEmpty && k < kBarKEmpty + kStagesK) || (k >= kBarVEmpty && k < kBarVEmpty + kStagesV)) count = 2;
       if (k >= kPtPieceEmpty) count = 11;
       mbar_init(bar(k), count);
@@ -256,7 +264,7 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
       uint32_t gt = 0;  // tiles of this head so far
       uint32_t np = 0;  // pieces this head had rows in
       uint32_t nq = 0;  // Q tiles asked for
-      const uint32_t tS = tmem + col_s(i), tO = tmem + col_o(i), tP = tmem + col_p(i, 0);
+      const uint32_t tS = tmem + col_sp(i, 0), tO = tmem + col_o(i);
       const uint32_t lo_q = desc_lo(sbase + kOff2Q + i * kTile2Bytes, 16);
       const uint32_t lo_k = desc_lo(sbase + kOff2K, 16), lo_v = desc_lo(sbase + kOff2V, 128 * 128);
       auto wait = [&](int slot, uint32_t parity) {
@@ -271,16 +279,21 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
                       bar(kPtQFull + i));
         ++nq;
       };
-      // S of half h of the K stage: 8 products of 16 columns
+      // S of half h of the K stage: 8 products of 16 columns.  What the softmax
+      // left in that buffer, P, was read by a product issued before
       auto qk = [&](int h) {
         tc_fence_after();
         const uint32_t k0 = lo_k + ks * (kTile2Bytes >> 4) + h * (kBk * 128 >> 4);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
           const uint32_t at = (kk >> 2) * (128 * 128 >> 4) + (kk & 3) * 2;
-          mma_ss(tS, lo_q + at, k0 + at, idesc_qk, kk > 0 ? 1u : 0u);
+          mma_ss(tS + kBk * h, lo_q + at, k0 + at, idesc_qk, kk > 0 ? 1u : 0u);
         }
-        tc_commit(bar(kBarSFull + i));
+        tc_commit(bar(kPtSFull + 2 * i + h));
+        if (h == 1) {
+          tc_commit(bar(kBarKEmpty + ks));
+          if (++ks == kStagesK) { ks = 0; kph ^= 1; }
+        }
       };
       // O (+)= P of half h times that half of the V stage: 4 products of 16 keys
       auto pv = [&](int h, bool add) {
@@ -288,11 +301,13 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
         const uint32_t v0 = lo_v + vs * (kTile2Bytes >> 4) + h * (kBk * 128 >> 4);
 #pragma unroll
         for (int kk = 0; kk < kBk / 16; ++kk)
-          mma_ts(tO, tP + 32 * h + 8 * kk, v0 + kk * (16 * 128 >> 4), idesc_pv, add || kk > 0 ? 1u : 0u);
+          mma_ts(tO, tS + kBk * h + 8 * kk, v0 + kk * (16 * 128 >> 4), idesc_pv, add || kk > 0 ? 1u : 0u);
         tc_commit(bar(kBarODone + 2 * i + h));
+        if (h == 1) {
+          tc_commit(bar(kBarVEmpty + vs));
+          if (++vs == kStagesV) { vs = 0; vph ^= 1; }
+        }
       };
-      auto leave_k = [&]() { if (++ks == kStagesK) { ks = 0; kph ^= 1; } };
-      auto leave_v = [&]() { if (++vs == kStagesV) { vs = 0; vph ^= 1; } };
       Piece p, next;
       ok = take_piece(0, next);
       if (ok) fetch_q(next);
@@ -305,48 +320,43 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
           for (int t = 0; ok && t < ntiles; ++t) {
             if (!wait(kBarKFull + ks, kph)) break;
             mbar_arrive(bar(kBarKEmpty + ks));
-            leave_k();
+            if (++ks == kStagesK) { ks = 0; kph ^= 1; }
             if (!wait(kBarVFull + vs, vph)) break;
             mbar_arrive(bar(kBarVEmpty + vs));
-            leave_v();
+            if (++vs == kStagesV) { vs = 0; vph ^= 1; }
           }
           if (ok) ok = take_piece(pi + 1, next);
           if (ok) fetch_q(next);
           continue;
         }
-        // chunk by chunk (half tiles): S of a chunk as soon as the softmax has
-        // read S of the one before, then P V of the one before.  The thread
-        // does little but issue: descriptors are a base plus constants, stages
-        // and parities are counted, since its instructions, one warp's chain,
-        // are what the tensor core waits for.
-        if (!wait(kPtQFull + i, np & 1)) break;
+        // half a tile at a time, two S buffers: P V of a half, then S of the same
+        // half of the next tile into its buffer, so the softmax finds its next
+        // scores ready.  The thread does little but issue: descriptors are a
+        // base plus constants, stages and parities are counted, since its
+        // instructions, one warp's chain, are what the tensor core waits for.
+        if (!wait(kPtQFull + i, np & 1) || !wait(kBarKFull + ks, kph)) break;
+        qk(0);
+        qk(1);
         for (int t = 0; t < ntiles; ++t, ++gt) {
-          if (!wait(kBarKFull + ks, kph)) break;
-          if (gt > 0 && !wait(kBarSEmpty + i, 1)) break;
-          qk(0);
-          if (t > 0) {
-            if (!wait(kBarPFull + 2 * i + 1, (gt - 1) & 1)) break;
-            pv(1, true);
-            tc_commit(bar(kBarVEmpty + vs));
-            leave_v();
-          }
-          if (!wait(kBarSEmpty + i, 0)) break;
-          qk(1);
-          tc_commit(bar(kBarKEmpty + ks));
-          leave_k();
+          const bool more = t + 1 < ntiles;
           if (!wait(kBarVFull + vs, vph) || !wait(kBarPFull + 2 * i, gt & 1)) break;
           // the accumulator of the piece before this one has been read
           if (t == 0 && np > 0 && !wait(kPtOFree + i, (np - 1) & 1)) break;
           pv(0, t > 0);
+          if (more) {
+            if (!wait(kBarKFull + ks, kph)) break;
+            qk(0);
+          }
+          if (!wait(kBarPFull + 2 * i + 1, gt & 1)) break;
+          if (!more) {  // the softmax took the last scores: Q is free for the next piece
+            ok = take_piece(pi + 1, next);
+            if (!ok) break;
+            fetch_q(next);
+          }
+          pv(1, true);
+          if (more) qk(1);
         }
-        if (!ok || !wait(kBarPFull + 2 * i + 1, (gt - 1) & 1)) break;
-        // the softmax took the last scores: Q is free for the next piece
-        ok = take_piece(pi + 1, next);
         if (!ok) break;
-        fetch_q(next);
-        pv(1, true);
-        tc_commit(bar(kBarVEmpty + vs));
-        leave_v();
         ++np;
       }
       if (!ok) set_error(kErrTimeout);
@@ -368,7 +378,6 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
     const int r = tid & 127;
     const int rt = r / g.G, rh = r - rt * g.G;  // token of the tile, head of the group
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + col_s(qi) + lane_base;
     const uint32_t tO = tmem + col_o(qi) + lane_base;
     bool ok = true;
     uint32_t gc = 0;
@@ -395,24 +404,19 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
         const int t = p.tile0 + (c >> 1);
         const bool pre = p.kind == 0 || t < p.np;
         const int vis = (pre ? see_pre - t * kPtKeys : see_own - (t - p.np) * kPtKeys) - kBk * (c & 1);
-        if (!warp_wait(bar(kBarSFull + qi), n & 1, kSpinLimit)) { ok = false; break; }
+        const uint32_t tS = tmem + col_sp(qi, c & 1) + lane_base;
+        if (!warp_wait(bar(kPtSFull + 2 * qi + (c & 1)), (n >> 1) & 1, kSpinLimit)) { ok = false; break; }
         tc_fence_after();
         if (idle) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(bar(kBarSEmpty + qi));
-            mbar_arrive(bar(kBarPFull + 2 * qi + (c & 1)));
-          }
+          if (lane == 0) mbar_arrive(bar(kBarPFull + 2 * qi + (c & 1)));
           continue;
         }
         float x[kBk];
         tmem_ld32(tS, x);
         tmem_ld32(tS + 32, x + 32);
         tc_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarSEmpty + qi));
         const bool full = vis >= kBk;
         // the largest score the row sees in this chunk, as a reference
         auto reference = [&]() {
@@ -477,7 +481,7 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
           exponentials();
         }
         ell += rs;
-        tmem_st32(tmem + col_p(qi, c & 1) + lane_base, pw);
+        tmem_st32(tS, pw);
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
