@@ -92,7 +92,7 @@ PagedPlan paged_plan(const s2o_cache_config* c) {
 }
 
 struct PagedWs {
-  int64_t* units;   // of the tile kernel, of the decode kernel
+  PagedHead* head;  // of the tile kernel, of the decode kernel
   int4* meta;
   SplitItem* split;
   PagedPart tile, decode;
@@ -107,7 +107,7 @@ PagedWs paged_layout(const s2o_cache_config* c, const PagedPlan& p, int n, void*
     return static_cast<void*>(q);
   };
   const size_t rows = (size_t)c->Tq * c->Hq;
-  w.units = static_cast<int64_t*>(take(256));
+  w.head = static_cast<PagedHead*>(take(2 * sizeof(PagedHead)));
   const int streams = n * (kPgWarps / p.R);  // workers of the decode kernel
   if (c->prefix_len == 0 || p.chunks) {  // whole items are the result
     w.split = static_cast<SplitItem*>(take((size_t)(p.chunks ? n : streams) * sizeof(SplitItem)));
@@ -290,6 +290,8 @@ s2o_status s2o_attention_paged(const s2o_cache_config* cfg, const uint16_t* Q, c
   a.Q = Q; a.O = O; a.lse = lse; a.meta = w.meta; a.split = w.split;
   a.out_f32 = out_dtype == S2O_OUT_F32;
   a.direct = cfg->prefix_len == 0 || p.chunks;
+  a.beside = p.tiles;
+  a.own_ns = p.R == 1 ? 700.f : (p.R == 2 ? 1000.f : 2000.f);
   CUtensorMap tmQ, tmK, tmV;
   const uint64_t rows = (uint64_t)cfg->num_pages * cfg->Hkv * cfg->page_size;
   const uint32_t box = (uint32_t)std::min(cfg->page_size, 64);
@@ -298,8 +300,9 @@ s2o_status s2o_attention_paged(const s2o_cache_config* cfg, const uint16_t* Q, c
     if (!encode_rows_map(&tmK, k_cache, rows, box) || !encode_rows_map(&tmV, v_cache, rows, box)) return S2O_ERR_CUDA;
     if (!encode_query_map(&tmQ, Q, cfg->Tq, cfg->Hq, g.G, kLq / g.G, fp16)) return S2O_ERR_CUDA;
     a.c = p.tile;
+    a.other = p.decode;
     a.part = w.tile;
-    a.units = w.units;
+    a.head = w.head;
     if ((fp16 ? launch_tile<true>(a, tmQ, tmK, tmV, n, s) : launch_tile<false>(a, tmQ, tmK, tmV, n, s)) != cudaSuccess)
       return S2O_ERR_CUDA;
     ++t_launches;
@@ -308,8 +311,9 @@ s2o_status s2o_attention_paged(const s2o_cache_config* cfg, const uint16_t* Q, c
     if (!encode_rows_map(&tmK, k_cache, rows, kPgSub) || !encode_rows_map(&tmV, v_cache, rows, kPgSub))
       return S2O_ERR_CUDA;
     a.c = p.decode;
+    a.other = p.tile;
     a.part = w.decode;
-    a.units = w.units + 1;
+    a.head = w.head + 1;
     // beside the tile kernel: neither reads what the other writes
     if ((fp16 ? launch_decode_r<true>(p.R, a, tmK, tmV, n, s, p.tiles)
               : launch_decode_r<false>(p.R, a, tmK, tmV, n, s, p.tiles)) != cudaSuccess)
@@ -319,17 +323,17 @@ s2o_status s2o_attention_paged(const s2o_cache_config* cfg, const uint16_t* Q, c
   JoinArgs j{};
   j.g = g;
   const int streams = n * (kPgWarps / p.R);
-  const JoinSide tile = {w.tile, p.tile, w.units, n}, decode = {w.decode, p.decode, w.units + 1, streams};
+  const JoinSide tile = {w.tile, p.tile, w.head, n}, decode = {w.decode, p.decode, w.head + 1, streams};
   j.prefix = p.tiles ? tile : decode;
   j.own = p.chunks ? tile : decode;
   j.meta = w.meta; j.split = w.split; j.O = O; j.lse = lse; j.out_f32 = a.out_f32;
   cudaError_t e;
   if (a.direct) {
-    const dim3 grid(j.own.n, (j.own.part.rows + 31) / 32);
-    e = launch_early(fp16 ? k_paged_join_split<true> : k_paged_join_split<false>, grid, 256, 0, s, true, j);
+    const dim3 grid(j.own.n, (j.own.part.rows + 15) / 16);
+    e = launch_early(fp16 ? k_paged_join_split<true> : k_paged_join_split<false>, grid, 32 * kJoinWarps, 0, s, true, j);
   } else {
-    const unsigned blocks = (unsigned)(((int64_t)cfg->Tq * cfg->Hq + 7) / 8);
-    e = launch_early(fp16 ? k_paged_join<true> : k_paged_join<false>, blocks, 256, 0, s, true, j);
+    const unsigned blocks = (unsigned)(((int64_t)cfg->Tq * cfg->Hq + kJoinWarps - 1) / kJoinWarps);
+    e = launch_early(fp16 ? k_paged_join<true> : k_paged_join<false>, blocks, 32 * kJoinWarps, 0, s, true, j);
   }
   if (e != cudaSuccess) return S2O_ERR_CUDA;
   ++t_launches;

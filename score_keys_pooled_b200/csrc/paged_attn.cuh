@@ -70,18 +70,27 @@ struct PagedPart {
   int rows;          // rows of a slot
 };
 
+// what a kernel tells the join: its units and its workers
+struct PagedHead {
+  int64_t units;
+  int64_t workers;
+};
+
 struct PagedArgs {
   PagedGeom g;
   PagedCut c;
+  PagedCut other;     // side by side: the other kernel's
   const uint16_t* Q;  // [Tq, Hq, 128]
   void* O;
   float* lse;         // [Tq, Hq] or null
   PagedPart part;
   int4* meta;         // [Tq, Hkv]: first and last share of the token's own item, its place in the tile (join of rows)
   SplitItem* split;   // [workers] (join of split items)
-  int64_t* units;     // total units of this kernel, for the join
+  PagedHead* head;
   int out_f32;
   int direct;         // whole items are the result (no other list of keys to join)
+  int beside;         // tile and decode kernel share the SMs
+  float own_ns;       // see decode_sms
 };
 
 // the outcome of a wait that every lane made, agreed on by the warp
@@ -186,9 +195,11 @@ __global__ void __launch_bounds__(32 * kPgWarps, 1)
     mbar_init(empty(lane), R);
     fence_mbar_init();
   }
-  Sched sc = sched_begin(g, a.c, C::kStreams, stream, reinterpret_cast<int64_t*>(sgen + C::kOffRed),
+  const OwnRun run = own_run(g, a.c, reinterpret_cast<int64_t*>(sgen + C::kOffRed));
+  const int ctas = a.beside ? decode_sms(g, a.other, batch_tokens(g), run.total, a.own_ns, gridDim.x) : (int)gridDim.x;
+  Sched sc = sched_begin(g, a.c, C::kStreams, stream, ctas, run,
                          reinterpret_cast<SchedFound*>(sgen + C::kOffRed + 34 * 8));
-  if (tid == 0 && blockIdx.x == 0) *a.units = sc.U;
+  if (tid == 0 && blockIdx.x == 0) *a.head = {sc.U, ctas * C::kStreams};
   __syncthreads();
 
   // ---- the stream's loads, by its first warp: stage by stage through the
@@ -438,8 +449,8 @@ __global__ void __launch_bounds__(32 * kPgWarps, 1)
 struct JoinSide {
   PagedPart part;
   PagedCut c;
-  const int64_t* units;
-  int n;              // workers of the kernel that wrote it
+  const PagedHead* head;  // of the kernel that wrote it
+  int n;              // its workers at most
 };
 
 struct JoinArgs {
@@ -466,6 +477,10 @@ __device__ __forceinline__ float warp_add(float x) {
   for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
+template <int N>
+struct Count {
+  static constexpr int value = N;
+};
 // cnt parts; lane l of a batch of 32 gets part l's (reference, sum) and
 // accumulators from part(j, acc); one that saw no key has (-inf, 0)
 template <class F>
@@ -481,11 +496,12 @@ __device__ __forceinline__ void add_parts(RowSum& s, int cnt, int lane, F part) 
     s.l = s.l * f + warp_add(ml.y * w);
     s.o = make_float4(s.o.x * f, s.o.y * f, s.o.z * f, s.o.w * f);
     const int n = min(32, cnt - base);
-    for (int k0 = 0; k0 < n; k0 += 8) {
-      float4 v[8];
-      float wk[8];
+    auto some = [&](int k0, auto batch) {
+      constexpr int B = decltype(batch)::value;
+      float4 v[B];
+      float wk[B];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < B; ++k) {
         wk[k] = __shfl_sync(0xffffffffu, w, k0 + k);
         const float4* a = reinterpret_cast<const float4*>(
             __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(acc), k0 + k));
@@ -493,10 +509,13 @@ __device__ __forceinline__ void add_parts(RowSum& s, int cnt, int lane, F part) 
         if (wk[k] != 0.f) v[k] = a[lane];  // lanes behind the last part have weight 0
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
+      for (int k = 0; k < B; ++k)
         s.o = make_float4(fmaf(v[k].x, wk[k], s.o.x), fmaf(v[k].y, wk[k], s.o.y), fmaf(v[k].z, wk[k], s.o.z),
                           fmaf(v[k].w, wk[k], s.o.w));
-    }
+    };
+    int k0 = 0;
+    for (; k0 + 8 < n; k0 += 16) some(k0, Count<16>());
+    for (; k0 < n; k0 += 8) some(k0, Count<8>());
   }
 }
 // part j of an item in shares c0 .. (member `offset` of teams of `stride`)
@@ -522,19 +541,22 @@ __device__ __forceinline__ void finish_row(const JoinArgs& a, const RowSum& s, s
   if (a.lse && lane == 0) a.lse[row] = lse_of(s.m, s.l);
 }
 
+constexpr int kJoinWarps = 4;
+
 // every row of the batch: its prefix parts and its own
 template <bool FP16>
-__global__ void __launch_bounds__(256) k_paged_join(const __grid_constant__ JoinArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps) k_paged_join(const __grid_constant__ JoinArgs a) {
   const PagedGeom& g = a.g;
   const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int row = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
   const int t = row / g.Hq, h = row - t * g.Hq;
   wait_for_previous();
   if (t >= g.Tq) return;
   const int ntok = batch_tokens(g);
   const int kvh = h / g.G, hh = h - kvh * g.G;
   int4 own = a.meta[(int64_t)t * g.Hkv + kvh];
-  const int64_t PU = *a.prefix.units;
+  const int64_t PU = a.prefix.head->units;
+  const int workers = max(1, min((int)a.prefix.head->workers, a.prefix.n));
   if (t >= ntok) return;
   own.x = max(0, min(own.x, a.own.n - 1));  // rows of a refused sequence were never written
   own.y = max(own.x, min(own.y, a.own.n - 1));
@@ -542,7 +564,7 @@ __global__ void __launch_bounds__(256) k_paged_join(const __grid_constant__ Join
   const PagedCut& c = a.prefix.c;
   const int npt = (ntok + c.tpt - 1) / c.tpt, rt = t / c.tpt;
   const int64_t np = ((int64_t)g.prefix + (1 << c.kt_log2) - 1) >> c.kt_log2;
-  const int team = team_size(c, npt, a.prefix.n), n = shares_of(PU, a.prefix.n / team);
+  const int team = team_size(c, npt, workers), n = shares_of(PU, workers / team);
   const int64_t u0 = (team > 1 ? (int64_t)kvh : (int64_t)kvh * npt + rt) * np;
   const int c0 = share_owner(PU, n, u0), c1 = share_owner(PU, n, u0 + np - 1);
   const int parts = c1 - c0 + 1, member = team > 1 ? rt : 0, prow = (t - rt * c.tpt) * g.G + hh;
@@ -560,12 +582,12 @@ __global__ void __launch_bounds__(256) k_paged_join(const __grid_constant__ Join
 // own items that two or more workers share (all others are the result already):
 // blocks (c, y) take the rows of the one that begins in share c and goes on
 template <bool FP16>
-__global__ void __launch_bounds__(256) k_paged_join_split(const __grid_constant__ JoinArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps) k_paged_join_split(const __grid_constant__ JoinArgs a) {
   const PagedGeom& g = a.g;
   wait_for_previous();
   const SplitItem it = a.split[blockIdx.x];
   const int lane = threadIdx.x & 31;
-  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < it.ntok * g.G; r += gridDim.y * 8) {
+  for (int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); r < it.ntok * g.G; r += gridDim.y * kJoinWarps) {
     const int t = r / g.G;
     RowSum s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
     add_parts(s, it.c1 - (int)blockIdx.x + 1, lane,

@@ -190,16 +190,76 @@ struct SchedFound {
   int seq;
   int64_t u;  // the sequence's first unit
 };
-// Block-wide (blockDim.x a multiple of 32, at most 1024 threads): total units
-// and the item of the first unit of this thread's share.  A block is `own`
-// workers (1 to 8), worker w of block b is number w * gridDim.x + b; the
-// calling thread asks for worker `which` of its block.  `red` (33 words) and `found` (`own`
-// entries) are in shared memory.
-__device__ __forceinline__ Sched sched_begin(const PagedGeom& g, const PagedCut& c, int own, int which, int64_t* red,
-                                             SchedFound* found) {
+// Units of all own items, and where this thread's run of sequences [s0, s1)
+// stands among them.  Block-wide, blockDim.x a multiple of 32 up to 1024;
+// `red` is 33 words of shared memory, free again after the next barrier.
+struct OwnRun {
+  int s0, s1;
+  int64_t begin, mine, total;
+};
+__device__ __forceinline__ OwnRun own_run(const PagedGeom& g, const PagedCut& c, int64_t* red) {
   const int tid = threadIdx.x, nth = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nth >> 5;
+  const int per = (g.nseq + nth - 1) / nth;
+  OwnRun r;
+  r.s0 = min(g.nseq, tid * per);
+  r.s1 = min(g.nseq, r.s0 + per);
+  r.mine = 0;
+  for (int q = r.s0; q < r.s1; ++q) {
+    const SeqInfo si = seq_info(g, q);
+    if (si.qlen > 0) {
+      const OwnUnits ou = own_units(si.qlen, si.len, g.prefix, c);
+      r.mine += g.Hkv * ou.before(ou.nrt);
+    }
+  }
+  int64_t incl = r.mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) red[warp] = incl;
+  __syncthreads();
+  // every warp adds up the sums of the warps before it
+  int64_t v = lane < nw ? red[lane] : 0, before = lane < warp ? v : 0;
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) {
+    v += __shfl_xor_sync(0xffffffffu, v, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  r.total = v;
+  r.begin = before + incl - r.mine;
+  return r;
+}
+
+// Prefix items in the tile kernel and own items in the decode kernel run side
+// by side: of `sms` SMs the decode kernel gets a share that makes both end
+// together.  A prefix unit (256 rows, 128 keys) keeps an SM 2250 ns busy (1300
+// with 128 rows); an own unit (64 keys, 32 KB) costs an SM of eight, four or
+// two streams 700, 1000 or 2000 ns (64 sequences of 512 keys behind 32K: 92, 84, 85, 99 us at 500,
+// 700, 900, 1200; one after the other on all SMs: 110).  Both kernels come to
+// the same answer.
+constexpr float kTileNs = 2250.f, kHalfTileNs = 1300.f;
+__device__ __forceinline__ int decode_sms(const PagedGeom& g, const PagedCut& tile, int ntok, int64_t own_units,
+                                          float own_ns, int sms) {
+  const int npt = (ntok + tile.tpt - 1) / tile.tpt;
+  const int64_t np = ((int64_t)g.prefix + (1 << tile.kt_log2) - 1) >> tile.kt_log2;
+  const float w1 = (float)((int64_t)npt * g.Hkv * np) * (2 * ntok <= tile.tpt ? kHalfTileNs : kTileNs);
+  const float w2 = (float)own_units * own_ns;
+  const int n = __float2int_rn((float)sms * w2 / (w1 + w2));
+  return max(1, min(sms - 1, n));
+}
+
+// Total units and the item of the first unit of this thread's share.  A block
+// is `own` workers (1 to 8), `ctas` of the grid's blocks work: worker w of
+// block b is number w * ctas + b; the calling thread asks for worker `which`
+// of its block.  `run`: own_run() of the block (without own items: unused).
+// `found` (`own` entries) is in shared memory.  Block-wide.
+__device__ __forceinline__ Sched sched_begin(const PagedGeom& g, const PagedCut& c, int own, int which, int ctas,
+                                             const OwnRun& run, SchedFound* found) {
+  const int tid = threadIdx.x;
   Sched s;
-  const int workers = gridDim.x * own, number = which * gridDim.x + blockIdx.x;
+  const int workers = ctas * own, number = which * ctas + blockIdx.x;
+  const bool works = blockIdx.x < ctas;
   s.ntok_all = batch_tokens(g);
   s.npt = c.prefix_items ? (s.ntok_all + c.tpt - 1) / c.tpt : 0;
   const int64_t np = ((int64_t)g.prefix + (1 << c.kt_log2) - 1) >> c.kt_log2;
@@ -208,7 +268,7 @@ __device__ __forceinline__ Sched sched_begin(const PagedGeom& g, const PagedCut&
     s.U = g.Hkv * np;
     s.n = shares_of(s.U, workers / s.team);
     s.me = number / s.team;
-    s.kind = s.me < s.n ? 0 : -1;
+    s.kind = works && s.me < s.n ? 0 : -1;
     s.seq = 0;
     if (s.kind < 0) return s;
     s.u = share_begin(s.U, s.n, s.me);
@@ -220,51 +280,20 @@ __device__ __forceinline__ Sched sched_begin(const PagedGeom& g, const PagedCut&
     return s;
   }
   const int64_t PU = (int64_t)s.npt * g.Hkv * np;
-  // units of this thread's run of sequences, and the exclusive sum over the block
-  const int per = (g.nseq + nth - 1) / nth;
-  const int s0 = min(g.nseq, tid * per), s1 = min(g.nseq, s0 + per);
-  int64_t mine = 0;
-  if (c.own_items)
-    for (int q = s0; q < s1; ++q) {
-      const SeqInfo si = seq_info(g, q);
-      if (si.qlen > 0) {
-        const OwnUnits ou = own_units(si.qlen, si.len, g.prefix, c);
-        mine += g.Hkv * ou.before(ou.nrt);
-      }
-    }
-  int64_t incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) red[warp] = incl;
   if (tid < own) found[tid].seq = g.nseq;
   __syncthreads();
-  if (warp == 0) {
-    int64_t v = lane < nw ? red[lane] : 0;
-    const int64_t own = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += y;
-    }
-    if (lane < nw) red[lane] = v - own;
-    if (lane == nw - 1) red[32] = v;
-  }
-  __syncthreads();
-  s.U = PU + red[32];
+  s.U = PU + (c.own_items ? run.total : 0);
   s.n = shares_of(s.U, workers);
   s.me = number;
-  const int64_t begin = PU + red[warp] + incl - mine;
   // the thread whose sequences hold a worker's first unit looks it up
-  for (int w = 0; w < own && mine > 0; ++w) {
-    const int me = w * gridDim.x + blockIdx.x;
+  const int64_t begin = PU + run.begin;
+  for (int w = 0; w < own && works && c.own_items && run.mine > 0; ++w) {
+    const int me = w * ctas + blockIdx.x;
     if (me >= s.n) break;
     const int64_t u = share_begin(s.U, s.n, me);
-    if (u < begin || u >= begin + mine) continue;
+    if (u < begin || u >= begin + run.mine) continue;
     int64_t at = begin;
-    for (int q = s0; q < s1; ++q) {
+    for (int q = run.s0; q < run.s1; ++q) {
       const SeqInfo si = seq_info(g, q);
       if (si.qlen == 0) continue;
       const OwnUnits ou = own_units(si.qlen, si.len, g.prefix, c);
@@ -278,7 +307,7 @@ __device__ __forceinline__ Sched sched_begin(const PagedGeom& g, const PagedCut&
     }
   }
   __syncthreads();
-  if (s.me >= s.n) {
+  if (!works || s.me >= s.n) {
     s.kind = -1;
     return s;
   }

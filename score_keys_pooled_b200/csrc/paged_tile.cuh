@@ -134,14 +134,17 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
   const int trows = tpt * g.G;    // its rows
 
   let_next_start();
-  if (tid == 0) {
-    for (int k = 0; k < kPtBars; ++k) {
-      uint32_t count = 1;
-      if ((k >= kBarPFull && k < kBarPFull + 4) || (k >= kPtOFree && k < kPtOFree + 2)) count = 4;
-      if ((k >= kBarKEmpty && k < kBarKEmpty + kStagesK) || (k >= kBarVEmpty && k < kBarVEmpty + kStagesV)) count = 2;
-      if (k >= kPtPieceEmpty) count = 11;
-      mbar_init(bar(k), count);
-    }
+  // side by side with the decode kernel: its items decide how many SMs are left
+  const OwnRun run = own_run(g, a.beside ? a.other : a.c, reinterpret_cast<int64_t*>(sgen + kPtOffRed));
+  const int ctas =
+      gridDim.x - (a.beside ? decode_sms(g, a.c, batch_tokens(g), run.total, a.own_ns, gridDim.x) : 0);
+  if (blockIdx.x >= ctas) return;  // an SM for the decode kernel
+  if (tid < kPtBars) {
+    uint32_t count = 1;
+    if ((tid >= kBarPFull && tid < kBarPFull + 4) || (tid >= kPtOFree && tid < kPtOFree + 2)) count = 4;
+    if ((tid >= kBarKEmpty && tid < kBarKEmpty + kStagesK) || (tid >= kBarVEmpty && tid < kBarVEmpty + kStagesV)) count = 2;
+    if (tid >= kPtPieceEmpty) count = 11;
+    mbar_init(bar(tid), count);
     fence_mbar_init();
   }
   // Q rows that no box fills (128 is no multiple of G): zero
@@ -155,9 +158,8 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
     tmem_alloc(smem_u32((const void*)tmem_slot), kTmem2Cols);
     tmem_relinquish();
   }
-  Sched sc = sched_begin(g, a.c, 1, 0, reinterpret_cast<int64_t*>(sgen + kPtOffRed),
-                         reinterpret_cast<SchedFound*>(sgen + kPtOffRed + 34 * 8));
-  if (tid == 0 && blockIdx.x == 0) *a.units = sc.U;
+  Sched sc = sched_begin(g, a.c, 1, 0, ctas, run, reinterpret_cast<SchedFound*>(sgen + kPtOffRed + 34 * 8));
+  if (tid == 0 && blockIdx.x == 0) *a.head = {sc.U, ctas};
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
