@@ -392,10 +392,12 @@ def _call_on(device, stream, fn, name, *args):
     import torch
     if device.type != "cuda":
         _refuse(f"{name}: the tensors are on {device}, not on a CUDA device")
-    if device.index != torch.cuda.current_device():
+    at = device.index
+    if at != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
             return _call_on(device, stream, fn, name, *args)
-    code = fn(*args, (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream)
+    # the raw handle: a Stream object costs 2 us, as much as the launch
+    code = fn(*args, torch._C._cuda_getCurrentRawStream(at) if stream is None else stream.cuda_stream)
     if code:
         raise S2OError(code, name)
 
@@ -413,24 +415,28 @@ def rotary(r: RotaryConfig, q, k, positions, q_out=None, k_out=None, inverse: bo
     B, N, dev, t = x.shape[0], x.shape[1], x.device, x.dtype
     if t is not torch.bfloat16 and t is not torch.float16:
         _refuse(f"rotary: {t} is neither bfloat16 nor float16")
-    sides = []
-    for name, src, dst in (("rotary: q", q, q_out), ("rotary: k", k, k_out)):
-        if src is None:
-            sides.append((0, None, None, None))
-            continue
-        if src.dim() != 4:
-            _refuse(f"{name} must be a [B, N, H, 128] tensor")
-        H = src.shape[2]
-        shape = (B, N, H, 128)
-        vin = _view4(src, name, shape, t, dev)
-        if dst is None:
-            dst = _empty(shape, t, dev, stream, None if inverse else (H * N * 128, 128, N * 128, 1))
-        sides.append((H, vin, _view4(dst, name + "_out", shape, t, dev), dst))
+    Hq, qi, qo, q_out = _turned("rotary: q", q, q_out, B, N, t, dev, inverse, stream)
+    Hkv, ki, ko, k_out = _turned("rotary: k", k, k_out, B, N, t, dev, inverse, stream)
     pos = _plain(positions, "rotary: positions", (r.naxes, B, N), torch.int32, dev)
-    (Hq, qi, qo, qd), (Hkv, ki, ko, kd) = sides
     _call_on(dev, stream, lib().s2o_rotary, "s2o_rotary", r, FP16 if t is torch.float16 else BF16, B, N, Hq, Hkv, qi,
              ki, pos, qo, ko, int(inverse))
-    return qd, kd
+    return q_out, k_out
+
+
+def _turned(name, src, dst, B, N, t, dev, inverse, stream):
+    """(heads, input view, output view, output) of one side of a rotation."""
+    if src is None:
+        return 0, None, None, None
+    if src.dim() != 4:
+        _refuse(f"{name} must be a [B, N, H, 128] tensor")
+    H = src.shape[2]
+    shape = (B, N, H, 128)
+    vin = _view4(src, name, shape, t, dev)
+    if dst is None:
+        strides = (H * N * 128, H * 128, 128, 1) if inverse else (H * N * 128, 128, N * 128, 1)
+        dst = _empty(shape, t, dev, stream, strides)
+        return H, vin, View(dst.data_ptr(), *strides[:3]), dst
+    return H, vin, _view4(dst, name + "_out", shape, t, dev), dst
 
 
 def alloc_cache(cfg: CacheConfig, device="cuda"):
