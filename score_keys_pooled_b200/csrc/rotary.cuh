@@ -25,8 +25,8 @@
 
 namespace s2o {
 
-constexpr int kRotThreads = 256;
-constexpr int kRotMaxTokens = 8;      // tokens of a block
+constexpr int kRotThreads = 128;      // 256 threads and 8 tokens: 78 us where this takes 76.5 (2 x 9973 tokens, 40 heads)
+constexpr int kRotMaxTokens = 4;      // tokens of a block
 constexpr unsigned kErrBadCache = 8u;  // device error word: page id, length or token range out of range
 
 struct RotaryTable {
@@ -74,15 +74,19 @@ __device__ __forceinline__ void fill_angles(float4 (*cs)[4][8], const RotaryTabl
 }
 
 // lane j of a row: both chunks of its eight pairs, turned; or copied
-template <bool FP16>
+// (STREAM: read and written past the caches' use, which the append's scattered
+// rows gain by, 72 -> 70 us for 14k tokens, and the rotation's lose by)
+template <bool FP16, bool STREAM>
 __device__ __forceinline__ void turn_row(const uint16_t* src, uint16_t* dst, int j, bool rotate, const RotaryTable& r,
                                          const float4 (*cs)[8]) {
   const bool turn = rotate && 16 * j < r.rot;
   // element offsets of the lane's two chunks
   const int e0 = turn && !r.adjacent ? 8 * j : 16 * j;
   const int e1 = turn && !r.adjacent ? 8 * j + (r.rot >> 1) : 16 * j + 8;
-  uint4 a = *reinterpret_cast<const uint4*>(src + e0);
-  uint4 b = *reinterpret_cast<const uint4*>(src + e1);
+  const uint4* s0 = reinterpret_cast<const uint4*>(src + e0);
+  const uint4* s1 = reinterpret_cast<const uint4*>(src + e1);
+  uint4 a = STREAM ? __ldcs(s0) : *s0;
+  uint4 b = STREAM ? __ldcs(s1) : *s1;
   if (turn) {
     uint32_t* aw = reinterpret_cast<uint32_t*>(&a);
     uint32_t* bw = reinterpret_cast<uint32_t*>(&b);
@@ -106,8 +110,15 @@ __device__ __forceinline__ void turn_row(const uint16_t* src, uint16_t* dst, int
       }
     }
   }
-  *reinterpret_cast<uint4*>(dst + e0) = a;
-  *reinterpret_cast<uint4*>(dst + e1) = b;
+  uint4* d0 = reinterpret_cast<uint4*>(dst + e0);
+  uint4* d1 = reinterpret_cast<uint4*>(dst + e1);
+  if (STREAM) {
+    __stcs(d0, a);
+    __stcs(d1, b);
+  } else {
+    *d0 = a;
+    *d1 = b;
+  }
 }
 
 struct RotaryArgs {
@@ -139,7 +150,7 @@ __global__ void __launch_bounds__(kRotThreads) k_rotary(const __grid_constant__ 
     const RowView& in = isq ? a.q : a.k;
     const RowView& out = isq ? a.qo : a.ko;
     const int hh = isq ? h : h - a.Hq;
-    turn_row<FP16>(in.p + b * in.sb + t * in.st + hh * in.sh, out.p + b * out.sb + t * out.st + hh * out.sh, j, true,
+    turn_row<FP16, false>(in.p + b * in.sb + t * in.st + hh * in.sh, out.p + b * out.sb + t * out.st + hh * out.sh, j, true,
                    a.r, cs[tok]);
   }
 }
@@ -204,7 +215,7 @@ __global__ void __launch_bounds__(kRotThreads) k_cache_append(const __grid_const
     const int tok = i / H, t = t0 + tok;
     int h = i - tok * H;
     if (h < Hq) {
-      turn_row<FP16>(a.q.p + t * a.q.st + h * a.q.sh, a.qo.p + t * a.qo.st + h * a.qo.sh, j, true, a.r, cs[tok]);
+      turn_row<FP16, true>(a.q.p + t * a.q.st + h * a.q.sh, a.qo.p + t * a.qo.st + h * a.qo.sh, j, true, a.r, cs[tok]);
       continue;
     }
     if (slot[tok] < 0) continue;
@@ -212,7 +223,7 @@ __global__ void __launch_bounds__(kRotThreads) k_cache_append(const __grid_const
     const bool isk = h < a.Hkv;
     if (!isk) h -= a.Hkv;
     const RowView& in = isk ? a.k : a.v;
-    turn_row<FP16>(in.p + t * in.st + h * in.sh, (isk ? a.kc : a.vc) + (slot[tok] + ((int64_t)h << a.page_log2)) * kD, j,
+    turn_row<FP16, true>(in.p + t * in.st + h * in.sh, (isk ? a.kc : a.vc) + (slot[tok] + ((int64_t)h << a.page_log2)) * kD, j,
                    isk, a.r, cs[tok]);
   }
 }
