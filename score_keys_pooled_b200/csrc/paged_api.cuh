@@ -65,29 +65,50 @@ int sm_count() {
 
 // The paged attention's kernels for a call: a rule on sizes the host knows, so
 // the workspace size and the launches agree.
+//
+// Rows of a sequence's new tokens (max_q G) up to 32 go to the decode kernel,
+// which reads the cache at 16 or 32 rows a key; more fill a tcgen05 tile well
+// enough (33 rows of 128 still keep up with the memory: 64 KB of keys in 1.3
+// us).  The prefix is then taken the cheapest of these ways, by what its units
+// cost (decode_sms has the figures; a join costs 5 us and 1.5 us a thousand
+// rows, a second kernel beside the first 10 us):
+//   walk    each own item begins with the prefix: nothing to join, but every
+//           sequence reads it (from L2)
+//   items   prefix items in the same kernel: read once per row tile
+//   tiles   (decode) prefix items in the tile kernel beside it
 struct PagedPlan {
-  bool chunks;   // the tile kernel takes everything: a sequence's new rows fill tiles by themselves
-  bool tiles;    // the tile kernel takes the prefix, the decode kernel the own keys
+  bool chunks;   // the tile kernel takes the own keys, otherwise the decode kernel
+  bool tiles;    // decode: the tile kernel takes the prefix beside it
+  bool direct;   // whole items are the result
   int R;         // row tiles of 16 of the decode kernel
   PagedCut tile, decode;
 };
-PagedPlan paged_plan(const s2o_cache_config* c) {
+PagedPlan paged_plan(const s2o_cache_config* c, int sms) {
   PagedPlan p{};
   const int G = c->Hq / c->Hkv;
-  const int64_t seq_rows = (int64_t)std::min(c->max_q, c->Tq) * G, all_rows = (int64_t)c->Tq * G;
-  p.chunks = seq_rows > 64;
-  p.tiles = !p.chunks && c->prefix_len > 0 && all_rows > 64;
+  const int64_t seq_rows = (int64_t)std::min(c->max_q, std::max(c->Tq, 1)) * G;
+  p.chunks = seq_rows > 32;
+  p.R = seq_rows <= 16 ? 1 : 2;
   p.tile.tpt = 2 * (kLq / G);
   p.tile.kt_log2 = 7;
-  p.tile.prefix_items = p.tiles;
-  p.tile.own_items = p.tile.walk_prefix = p.chunks;
-  const int64_t rows = !p.tiles && c->prefix_len > 0 ? all_rows : seq_rows;
-  p.R = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
-  if (16 * p.R < G) p.R = G <= 32 ? 2 : 4;
-  p.decode.tpt = 16 * p.R / G;
+  p.decode.tpt = std::max(1, 16 * p.R / G);
   p.decode.kt_log2 = 6;
-  p.decode.prefix_items = c->prefix_len > 0 && !p.tiles;
-  p.decode.own_items = 1;
+  PagedCut& own = p.chunks ? p.tile : p.decode;
+  own.own_items = 1;
+  // microseconds
+  const double prefix = c->prefix_len, tokens = c->Tq, seqs = std::min(c->nseq, std::max(c->Tq, 1));
+  const double units = c->Hkv * std::ceil(prefix / (1 << own.kt_log2)) / sms;
+  const double unit = p.chunks ? (2 * c->max_q <= p.tile.tpt ? 1.3 : 2.25) : (p.R == 1 ? 0.6 : 0.9);
+  const double join = 5 + 1.5e-3 * tokens * c->Hq;
+  const double walk = units * unit * (seqs + std::floor(tokens / own.tpt));
+  const double items = units * (p.chunks ? 2.25 : unit) * std::ceil(tokens / own.tpt) + join;
+  const double tiles = p.chunks ? INFINITY
+                                : c->Hkv * std::ceil(prefix / 128) / sms * std::ceil(tokens / p.tile.tpt) * 2.25 + join + 10;
+  p.direct = c->prefix_len == 0 || (walk <= items && walk <= tiles);
+  p.tiles = !p.direct && tiles < items;
+  own.walk_prefix = p.direct && c->prefix_len > 0;
+  own.prefix_items = !p.direct && !p.tiles;
+  p.tile.prefix_items |= p.tiles;
   return p;
 }
 
@@ -98,6 +119,9 @@ struct PagedWs {
   PagedPart tile, decode;
   size_t bytes;
 };
+// workers of the kernel that takes the own keys
+int own_workers(const PagedPlan& p, int sms) { return p.chunks ? sms : sms * (kPgWarps / p.R); }
+
 PagedWs paged_layout(const s2o_cache_config* c, const PagedPlan& p, int n, void* base) {
   PagedWs w{};
   size_t off = 0;
@@ -108,9 +132,8 @@ PagedWs paged_layout(const s2o_cache_config* c, const PagedPlan& p, int n, void*
   };
   const size_t rows = (size_t)c->Tq * c->Hq;
   w.head = static_cast<PagedHead*>(take(2 * sizeof(PagedHead)));
-  const int streams = n * (kPgWarps / p.R);  // workers of the decode kernel
-  if (c->prefix_len == 0 || p.chunks) {  // whole items are the result
-    w.split = static_cast<SplitItem*>(take((size_t)(p.chunks ? n : streams) * sizeof(SplitItem)));
+  if (p.direct) {
+    w.split = static_cast<SplitItem*>(take((size_t)own_workers(p, n) * sizeof(SplitItem)));
   } else {
     w.meta = static_cast<int4*>(take((size_t)c->Tq * c->Hkv * sizeof(int4)));
     for (int k = 0; k < 2; ++k) {
@@ -125,7 +148,7 @@ PagedWs paged_layout(const s2o_cache_config* c, const PagedPlan& p, int n, void*
     part.slots_ml = static_cast<float2*>(take((size_t)2 * workers * r * sizeof(float2)));
   };
   if (p.chunks || p.tiles) slots(w.tile, n, 2 * kLq);
-  if (!p.chunks) slots(w.decode, streams, 16 * p.R);
+  if (!p.chunks) slots(w.decode, own_workers(p, n), 16 * p.R);
   w.bytes = off;
   return w;
 }
@@ -183,8 +206,7 @@ cudaError_t launch_decode(const PagedArgs& a, const CUtensorMap& k, const CUtens
 template <bool FP16>
 cudaError_t launch_decode_r(int R, const PagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, int n,
                             cudaStream_t s, bool early) {
-  return R == 1 ? launch_decode<FP16, 1>(a, k, v, n, s, early)
-                : (R == 2 ? launch_decode<FP16, 2>(a, k, v, n, s, early) : launch_decode<FP16, 4>(a, k, v, n, s, early));
+  return R == 1 ? launch_decode<FP16, 1>(a, k, v, n, s, early) : launch_decode<FP16, 2>(a, k, v, n, s, early);
 }
 
 }  // namespace
@@ -257,7 +279,8 @@ s2o_status s2o_attention_paged_workspace_size(const s2o_cache_config* cfg, size_
   s2o_status st = check_cache(cfg);
   if (st != S2O_OK) return st;
   if (!bytes) return S2O_ERR_INVALID_ARG;
-  *bytes = paged_layout(cfg, paged_plan(cfg), sm_count(), nullptr).bytes;
+  const int n = sm_count();
+  *bytes = paged_layout(cfg, paged_plan(cfg, n), n, nullptr).bytes;
   return S2O_OK;
 }
 
@@ -276,7 +299,7 @@ s2o_status s2o_attention_paged(const s2o_cache_config* cfg, const uint16_t* Q, c
       (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return S2O_ERR_INVALID_ARG;
   const int n = sm_count();
-  const PagedPlan p = paged_plan(cfg);
+  const PagedPlan p = paged_plan(cfg, n);
   const PagedWs w = paged_layout(cfg, p, n, workspace);
   if (workspace_bytes < w.bytes) return S2O_ERR_WORKSPACE_TOO_SMALL;
   if (cfg->Tq == 0) return S2O_OK;
@@ -289,9 +312,9 @@ s2o_status s2o_attention_paged(const s2o_cache_config* cfg, const uint16_t* Q, c
   g.prefix = cfg->prefix_len;
   a.Q = Q; a.O = O; a.lse = lse; a.meta = w.meta; a.split = w.split;
   a.out_f32 = out_dtype == S2O_OUT_F32;
-  a.direct = cfg->prefix_len == 0 || p.chunks;
+  a.direct = p.direct;
   a.beside = p.tiles;
-  a.own_ns = p.R == 1 ? 700.f : (p.R == 2 ? 1000.f : 2000.f);
+  a.own_ns = p.R == 1 ? 700.f : 1000.f;
   CUtensorMap tmQ, tmK, tmV;
   const uint64_t rows = (uint64_t)cfg->num_pages * cfg->Hkv * cfg->page_size;
   const uint32_t box = (uint32_t)std::min(cfg->page_size, 64);
@@ -322,10 +345,9 @@ s2o_status s2o_attention_paged(const s2o_cache_config* cfg, const uint16_t* Q, c
   }
   JoinArgs j{};
   j.g = g;
-  const int streams = n * (kPgWarps / p.R);
-  const JoinSide tile = {w.tile, p.tile, w.head, n}, decode = {w.decode, p.decode, w.head + 1, streams};
-  j.prefix = p.tiles ? tile : decode;
+  const JoinSide tile = {w.tile, p.tile, w.head, n}, decode = {w.decode, p.decode, w.head + 1, own_workers(p, n)};
   j.own = p.chunks ? tile : decode;
+  j.prefix = p.tiles ? tile : j.own;
   j.meta = w.meta; j.split = w.split; j.O = O; j.lse = lse; j.out_f32 = a.out_f32;
   cudaError_t e;
   if (a.direct) {
@@ -333,7 +355,9 @@ s2o_status s2o_attention_paged(const s2o_cache_config* cfg, const uint16_t* Q, c
     e = launch_early(fp16 ? k_paged_join_split<true> : k_paged_join_split<false>, grid, 32 * kJoinWarps, 0, s, true, j);
   } else {
     const unsigned blocks = (unsigned)(((int64_t)cfg->Tq * cfg->Hq + kJoinWarps - 1) / kJoinWarps);
-    e = launch_early(fp16 ? k_paged_join<true> : k_paged_join<false>, blocks, 32 * kJoinWarps, 0, s, true, j);
+    const bool many = (int64_t)cfg->Tq * cfg->Hq > (int64_t)n * 4 * kJoinWarps;  // more than one wave of the other form
+    e = launch_early(fp16 ? (many ? k_paged_join<true, true> : k_paged_join<true, false>)
+                          : (many ? k_paged_join<false, true> : k_paged_join<false, false>), blocks, 32 * kJoinWarps, 0, s, true, j);
   }
   if (e != cudaSuccess) return S2O_ERR_CUDA;
   ++t_launches;

@@ -142,6 +142,23 @@ __device__ __forceinline__ float lse_of(float ref, float sum) {
   return sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
 }
 
+// A piece's keys are at most two runs of a page list: the prefix's tiles, then
+// the sequence's own.  Run k (0 prefix, 1 own) in 16-key parts; `len` keys of
+// the list can be reached by the rows.
+struct KeyRun {
+  int sub0, sub1, len;
+};
+__device__ __forceinline__ KeyRun key_run(const PagedGeom& g, const Piece& p, int k) {
+  KeyRun r;
+  const bool pre = p.kind == 0;
+  const int t0 = k == 0 ? p.tile0 : (pre ? 0 : max(p.tile0 - p.np, 0));
+  const int t1 = k == 0 ? (pre ? p.tile1 : min(p.tile1, p.np)) : (pre ? 0 : p.tile1 - p.np);
+  r.len = k == 0 ? g.prefix : p.len;
+  r.sub0 = t0 * (kPgKeys / kPgSub);
+  r.sub1 = t1 > t0 ? (min(r.len, t1 * kPgKeys) + kPgSub - 1) / kPgSub : r.sub0;
+  return r;
+}
+
 // the page of a box of keys: clamped and flagged when it is none of the cache's
 __device__ __forceinline__ int checked_page(const PagedGeom& g, const int32_t* list, int64_t i) {
   const int p = list[i];
@@ -207,8 +224,9 @@ __global__ void __launch_bounds__(32 * kPgWarps, 1)
   // first stage; the end is a piece of kind -1 with a stage that loads nothing.
   // A piece holds at least one stage, so a slot is read before it comes round.
   uint32_t put = 0, pieces_put = 0;     // stages and pieces announced
-  int sub = 0, sub1 = 0, base = 0;      // next and last 16 keys of the piece; first of the lanes' pages
+  int sub = 0, sub1 = 0, base = 0;      // next and last 16 keys of the run; first of the lanes' pages
   int page = 0, page_next = 0;          // page of 16 keys base + lane, and of the 32 behind
+  int keys = 1;                         // run of the piece
   Piece ip;
   ip.kind = 0;
   const int32_t* list = nullptr;
@@ -224,20 +242,24 @@ __global__ void __launch_bounds__(32 * kPgWarps, 1)
         return;
       }
     }
-    if (sub == sub1) {
-      ip = sched_next(g, a.c, sc);
-      if (lane == 0) *piece_at(pieces_put) = ip;
-      ++pieces_put;
-      announce_split(a, sc, ip, split, lane);
-      if (ip.kind < 0) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full(st));
-        ++put;
-        return;
+    while (sub == sub1) {  // the next run, of this piece or the next
+      if (++keys == 2) {
+        ip = sched_next(g, a.c, sc);
+        if (lane == 0) *piece_at(pieces_put) = ip;
+        ++pieces_put;
+        announce_split(a, sc, ip, split, lane);
+        if (ip.kind < 0) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full(st));
+          ++put;
+          return;
+        }
+        keys = 0;
       }
-      list = ip.kind == 0 ? g.prefix_pages : g.table + (int64_t)ip.seq * g.max_pages;
-      sub = base = ip.tile0 * (kPgKeys / kPgSub);
-      sub1 = (min(ip.len, ip.tile1 * kPgKeys) + kPgSub - 1) / kPgSub;
+      const KeyRun r = key_run(g, ip, keys);
+      list = keys == 0 ? g.prefix_pages : g.table + (int64_t)ip.seq * g.max_pages;
+      sub = base = r.sub0;
+      sub1 = r.sub1;
       page = sub + lane < sub1 ? checked_page(g, list, (sub + lane) >> sub_log2) : 0;
       page_next = sub + 32 + lane < sub1 ? checked_page(g, list, (sub + 32 + lane) >> sub_log2) : 0;
     }
@@ -271,10 +293,8 @@ __global__ void __launch_bounds__(32 * kPgWarps, 1)
     if (p.kind < 0) break;
     const int rows = p.ntok * g.G;
     const bool active = 16 * rt < rows;
-    const int sub0 = p.tile0 * (kPgKeys / kPgSub);
-    const int subn = (min(p.len, p.tile1 * kPgKeys) + kPgSub - 1) / kPgSub;
     // this lane's rows: r0 and r0 + 8 of the warp's 16
-    int lim[2];       // keys < lim are seen
+    int lim_own[2];   // own keys < lim_own are seen
     size_t orow[2];   // row of [Tq, Hq]
     bool has[2];
     uint32_t qf[8][4];
@@ -283,7 +303,7 @@ __global__ void __launch_bounds__(32 * kPgWarps, 1)
       const int r = 16 * rt + r0 + 8 * k;
       has[k] = r < rows;
       const int tt = has[k] ? r / g.G : 0, h = has[k] ? r - tt * g.G : 0;
-      lim[k] = !has[k] ? 0 : (p.kind == 0 ? p.len : p.off + tt + 1);
+      lim_own[k] = has[k] ? p.off + tt + 1 : 0;
       orow[k] = (size_t)(p.tok0 + tt) * g.Hq + p.kvh * g.G + h;
       const uint16_t* q = a.Q + orow[k] * kD + cq;
 #pragma unroll
@@ -299,7 +319,10 @@ __global__ void __launch_bounds__(32 * kPgWarps, 1)
       for (int k = 0; k < 4; ++k) acc[n][k] = 0.f;
     float ref[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
 
-    for (int t = sub0; t < subn; ++t, ++it) {
+    for (int keys = 0; keys < 2; ++keys) {
+    const KeyRun r = key_run(g, p, keys);
+    const int lim[2] = {keys == 0 ? (has[0] ? r.len : 0) : lim_own[0], keys == 0 ? (has[1] ? r.len : 0) : lim_own[1]};
+    for (int t = r.sub0; t < r.sub1; ++t, ++it) {
       const int st = it % C::kStages;
       if (!warp_ok(mbar_wait_bounded(full(st), (it / C::kStages) & 1))) { ok = false; break; }
       if (active) {
@@ -363,12 +386,12 @@ __global__ void __launch_bounds__(32 * kPgWarps, 1)
             pf[2 * n + 1] = pack2<FP16>(p2, p3);
           }
         }
-        if (key0 + kPgSub > p.len) {
+        if (key0 + kPgSub > r.len) {
           // V rows behind the list: zero (the stream's other warps write the
           // same zeros); before the stage's next TMA write, a proxy fence
           for (int i = lane; i < kPgSub * 16; i += 32) {
             const int row = i >> 4, ch = i & 15;
-            if (key0 + row >= p.len)
+            if (key0 + row >= r.len)
               *reinterpret_cast<uint4*>(sgen + (sV - sbase) + (ch >> 3) * (kPgSub * 128) + swz128(row, ch & 7)) =
                   make_uint4(0, 0, 0, 0);
           }
@@ -393,6 +416,8 @@ __global__ void __launch_bounds__(32 * kPgWarps, 1)
       // the one before, which they have left by now
       if (rt == 0 && (R == 1 || it > 0)) issue();
       if (!ok) break;
+    }
+    if (!ok) break;
     }
     if (!ok) break;
     if (!active) continue;
@@ -483,7 +508,7 @@ struct Count {
 };
 // cnt parts; lane l of a batch of 32 gets part l's (reference, sum) and
 // accumulators from part(j, acc); one that saw no key has (-inf, 0)
-template <class F>
+template <bool MANY, class F>
 __device__ __forceinline__ void add_parts(RowSum& s, int cnt, int lane, F part) {
   for (int base = 0; base < cnt; base += 32) {
     const float* acc = nullptr;
@@ -514,8 +539,12 @@ __device__ __forceinline__ void add_parts(RowSum& s, int cnt, int lane, F part) 
                           fmaf(v[k].w, wk[k], s.o.w));
     };
     int k0 = 0;
-    for (; k0 + 8 < n; k0 += 16) some(k0, Count<16>());
-    for (; k0 < n; k0 += 8) some(k0, Count<8>());
+    if constexpr (MANY) {
+      for (; k0 < n; k0 += 4) some(k0, Count<4>());
+    } else {
+      for (; k0 + 8 < n; k0 += 16) some(k0, Count<16>());
+      for (; k0 < n; k0 += 8) some(k0, Count<8>());
+    }
   }
 }
 // part j of an item in shares c0 .. (member `offset` of teams of `stride`)
@@ -543,9 +572,11 @@ __device__ __forceinline__ void finish_row(const JoinArgs& a, const RowSum& s, s
 
 constexpr int kJoinWarps = 4;
 
-// every row of the batch: its prefix parts and its own
-template <bool FP16>
-__global__ void __launch_bounds__(32 * kJoinWarps) k_paged_join(const __grid_constant__ JoinArgs a) {
+// Every row of the batch: its prefix parts and its own.  MANY: so many rows
+// that warps hide each other's trips to memory, so the registers go to more
+// warps instead of more loads in flight.
+template <bool FP16, bool MANY>
+__global__ void __launch_bounds__(32 * kJoinWarps, MANY ? 8 : 4) k_paged_join(const __grid_constant__ JoinArgs a) {
   const PagedGeom& g = a.g;
   const int lane = threadIdx.x & 31;
   const int row = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
@@ -569,7 +600,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_paged_join(const __grid_con
   const int c0 = share_owner(PU, n, u0), c1 = share_owner(PU, n, u0 + np - 1);
   const int parts = c1 - c0 + 1, member = team > 1 ? rt : 0, prow = (t - rt * c.tpt) * g.G + hh;
   RowSum s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-  add_parts(s, parts + own.y - own.x + 1, lane, [&](int j, const float*& acc) {
+  add_parts<MANY>(s, parts + own.y - own.x + 1, lane, [&](int j, const float*& acc) {
     if (j < parts)
       return parts == 1 ? dense_part(a.prefix.part, 0, row, acc)
                         : split_part(a.prefix.part, c0, j, team, member, prow, acc);
@@ -590,7 +621,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_paged_join_split(const __gr
   for (int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); r < it.ntok * g.G; r += gridDim.y * kJoinWarps) {
     const int t = r / g.G;
     RowSum s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    add_parts(s, it.c1 - (int)blockIdx.x + 1, lane,
+    add_parts<false>(s, it.c1 - (int)blockIdx.x + 1, lane,
               [&](int j, const float*& acc) { return split_part(a.own.part, blockIdx.x, j, 1, 0, r, acc); });
     finish_row<FP16>(a, s, (size_t)(it.tok0 + t) * g.Hq + it.kvh * g.G + (r - t * g.G), lane);
   }

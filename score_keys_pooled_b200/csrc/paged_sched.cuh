@@ -234,8 +234,8 @@ __device__ __forceinline__ OwnRun own_run(const PagedGeom& g, const PagedCut& c,
 // Prefix items in the tile kernel and own items in the decode kernel run side
 // by side: of `sms` SMs the decode kernel gets a share that makes both end
 // together.  A prefix unit (256 rows, 128 keys) keeps an SM 2250 ns busy (1300
-// with 128 rows); an own unit (64 keys, 32 KB) costs an SM of eight, four or
-// two streams 700, 1000 or 2000 ns (64 sequences of 512 keys behind 32K: 92, 84, 85, 99 us at 500,
+// with 128 rows); an own unit (64 keys, 32 KB) costs an SM of eight or four
+// streams 700 or 1000 ns (64 sequences of 512 keys behind 32K: 92, 84, 85, 99 us at 500,
 // 700, 900, 1200; one after the other on all SMs: 110).  Both kernels come to
 // the same answer.
 constexpr float kTileNs = 2250.f, kHalfTileNs = 1300.f;
