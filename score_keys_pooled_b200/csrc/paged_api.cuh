@@ -132,10 +132,9 @@ PagedWs paged_layout(const s2o_cache_config* c, const PagedPlan& p, int n, void*
   };
   const size_t rows = (size_t)c->Tq * c->Hq;
   w.head = static_cast<PagedHead*>(take(2 * sizeof(PagedHead)));
-  if (p.direct) {
-    w.split = static_cast<SplitItem*>(take((size_t)own_workers(p, n) * sizeof(SplitItem)));
-  } else {
-    w.meta = static_cast<int4*>(take((size_t)c->Tq * c->Hkv * sizeof(int4)));
+  if (p.direct && p.chunks) w.split = static_cast<SplitItem*>(take((size_t)n * sizeof(SplitItem)));
+  else w.meta = static_cast<int4*>(take((size_t)c->Tq * c->Hkv * sizeof(int4)));
+  if (!p.direct) {
     for (int k = 0; k < 2; ++k) {
       w.decode.dense[k] = static_cast<float*>(take(rows * kD * sizeof(float)));
       w.decode.dense_ml[k] = static_cast<float2*>(take(rows * sizeof(float2)));
@@ -349,13 +348,15 @@ s2o_status s2o_attention_paged(const s2o_cache_config* cfg, const uint16_t* Q, c
   j.own = p.chunks ? tile : decode;
   j.prefix = p.tiles ? tile : j.own;
   j.meta = w.meta; j.split = w.split; j.O = O; j.lse = lse; j.out_f32 = a.out_f32;
+  j.direct = p.direct;
   cudaError_t e;
-  if (a.direct) {
-    const dim3 grid(j.own.n, (j.own.part.rows + 15) / 16);
+  if (w.split) {
+    const dim3 grid(n, 32);
     e = launch_early(fp16 ? k_paged_join_split<true> : k_paged_join_split<false>, grid, 32 * kJoinWarps, 0, s, true, j);
   } else {
-    const unsigned blocks = (unsigned)(((int64_t)cfg->Tq * cfg->Hq + kJoinWarps - 1) / kJoinWarps);
-    const bool many = (int64_t)cfg->Tq * cfg->Hq > (int64_t)n * 4 * kJoinWarps;  // more than one wave of the other form
+    const int64_t nrows = (int64_t)cfg->Tq * cfg->Hq;
+    const bool many = nrows > (int64_t)n * 8;  // more than one wave of a block each
+    const unsigned blocks = (unsigned)(many ? (nrows + kJoinWarps - 1) / kJoinWarps : nrows);
     e = launch_early(fp16 ? (many ? k_paged_join<true, true> : k_paged_join<true, false>)
                           : (many ? k_paged_join<false, true> : k_paged_join<false, false>), blocks, 32 * kJoinWarps, 0, s, true, j);
   }

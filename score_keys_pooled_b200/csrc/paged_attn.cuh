@@ -84,8 +84,9 @@ struct PagedArgs {
   void* O;
   float* lse;         // [Tq, Hq] or null
   PagedPart part;
-  int4* meta;         // [Tq, Hkv]: first and last share of the token's own item, its place in the tile (join of rows)
-  SplitItem* split;   // [workers] (join of split items)
+  // where the join finds the parts of own items, one of the two:
+  int4* meta;         // [Tq, Hkv]: first and last share of the token's item, its place in the tile
+  SplitItem* split;   // [workers]: the item that begins in a share and goes on
   PagedHead* head;
   int out_f32;
   int direct;         // whole items are the result (no other list of keys to join)
@@ -169,21 +170,21 @@ __device__ __forceinline__ int checked_page(const PagedGeom& g, const int32_t* l
   return p;
 }
 
-// Where the join finds the rows of an own item.  With the result written
-// directly only split items are joined: one record a CTA, written at the end
-// of its share.
+// Tells the join where the rows of an own item are: per token, or (chunks, whose
+// rows are many and whose items are seldom split) one record a share, written
+// at its end.
 __device__ __forceinline__ void announce_split(const PagedArgs& a, const Sched& sc, const Piece& p, SplitItem& split,
                                                int lane) {
   if (p.kind == 1 && p.first) {
-    const int me = sc.me;
-    const int c1 = p.last ? me : split_end(sc);
-    if (!a.direct) {
-      for (int t = lane; t < p.ntok; t += 32) a.meta[(int64_t)(p.tok0 + t) * a.g.Hkv + p.kvh] = make_int4(me, c1, t, 0);
+    const int c1 = p.last ? sc.me : split_end(sc);
+    if (a.meta) {
+      for (int t = lane; t < p.ntok; t += 32)
+        a.meta[(int64_t)(p.tok0 + t) * a.g.Hkv + p.kvh] = make_int4(sc.me, c1, t, 0);
     } else if (!p.last) {
       split = {p.tok0, p.ntok, p.kvh, c1};
     }
   }
-  if (p.kind < 0 && a.direct && lane == 0) a.split[sc.me] = split;
+  if (p.kind < 0 && a.split && lane == 0) a.split[sc.me] = split;
 }
 
 template <bool FP16, int R>
@@ -450,7 +451,6 @@ __global__ void __launch_bounds__(32 * kPgWarps, 1)
   }
   if (!ok && lane == 0) {
     set_error(kErrTimeout);
-    if (a.direct && rt == 0) a.split[stream * gridDim.x + blockIdx.x] = {0, 0, 0, 0};
   }
   // nothing may land in shared memory after the CTA ends
   if (rt == 0)
@@ -486,6 +486,7 @@ struct JoinArgs {
   void* O;
   float* lse;
   int out_f32;
+  int direct;         // no prefix items, and what was not split is the result
 };
 
 struct RowSum {
@@ -502,13 +503,10 @@ __device__ __forceinline__ float warp_add(float x) {
   for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
-template <int N>
-struct Count {
-  static constexpr int value = N;
-};
 // cnt parts; lane l of a batch of 32 gets part l's (reference, sum) and
-// accumulators from part(j, acc); one that saw no key has (-inf, 0)
-template <bool MANY, class F>
+// accumulators from part(j, acc); one that saw no key has (-inf, 0).  B loads
+// of accumulators are in flight at a time.
+template <int B, class F>
 __device__ __forceinline__ void add_parts(RowSum& s, int cnt, int lane, F part) {
   for (int base = 0; base < cnt; base += 32) {
     const float* acc = nullptr;
@@ -521,8 +519,7 @@ __device__ __forceinline__ void add_parts(RowSum& s, int cnt, int lane, F part) 
     s.l = s.l * f + warp_add(ml.y * w);
     s.o = make_float4(s.o.x * f, s.o.y * f, s.o.z * f, s.o.w * f);
     const int n = min(32, cnt - base);
-    auto some = [&](int k0, auto batch) {
-      constexpr int B = decltype(batch)::value;
+    for (int k0 = 0; k0 < n; k0 += B) {
       float4 v[B];
       float wk[B];
 #pragma unroll
@@ -537,15 +534,43 @@ __device__ __forceinline__ void add_parts(RowSum& s, int cnt, int lane, F part) 
       for (int k = 0; k < B; ++k)
         s.o = make_float4(fmaf(v[k].x, wk[k], s.o.x), fmaf(v[k].y, wk[k], s.o.y), fmaf(v[k].z, wk[k], s.o.z),
                           fmaf(v[k].w, wk[k], s.o.w));
-    };
-    int k0 = 0;
-    if constexpr (MANY) {
-      for (; k0 < n; k0 += 4) some(k0, Count<4>());
-    } else {
-      for (; k0 + 8 < n; k0 += 16) some(k0, Count<16>());
-      for (; k0 < n; k0 += 8) some(k0, Count<8>());
     }
   }
+}
+// A block's four warps on one row: warp w takes the parts w, w + 4, ... and
+// the first adds the four sums, in order.  Few rows have many parts (one for
+// each share of their item), and a warp would read them in turns.
+constexpr int kJoinWarps = 4;
+struct JoinShared {
+  float m[kJoinWarps], l[kJoinWarps];
+  float4 o[kJoinWarps][32];
+};
+template <class F>
+__device__ __forceinline__ RowSum block_add_parts(JoinShared& sh, int cnt, int warp, int lane, F part) {
+  RowSum s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  add_parts<8>(s, (cnt - warp + kJoinWarps - 1) / kJoinWarps, lane,
+               [&](int j, const float*& acc) { return part(kJoinWarps * j + warp, acc); });
+  if (lane == 0) {
+    sh.m[warp] = s.m;
+    sh.l[warp] = s.l;
+  }
+  sh.o[warp][lane] = s.o;
+  __syncthreads();
+  if (warp == 0) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, sh.m[w]);
+    s = {m, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      const float f = sh.m[w] == -INFINITY && sh.l[w] == 0.f ? 0.f : ex2_approx(sh.m[w] - m);
+      const float4 v = sh.o[w][lane];
+      s.l = fmaf(sh.l[w], f, s.l);
+      if (f != 0.f)
+        s.o = make_float4(fmaf(v.x, f, s.o.x), fmaf(v.y, f, s.o.y), fmaf(v.z, f, s.o.z), fmaf(v.w, f, s.o.w));
+    }
+  }
+  return s;
 }
 // part j of an item in shares c0 .. (member `offset` of teams of `stride`)
 __device__ __forceinline__ float2 split_part(const PagedPart& part, int c0, int j, int stride, int offset,
@@ -570,59 +595,71 @@ __device__ __forceinline__ void finish_row(const JoinArgs& a, const RowSum& s, s
   if (a.lse && lane == 0) a.lse[row] = lse_of(s.m, s.l);
 }
 
-constexpr int kJoinWarps = 4;
-
-// Every row of the batch: its prefix parts and its own.  MANY: so many rows
-// that warps hide each other's trips to memory, so the registers go to more
-// warps instead of more loads in flight.
+// Every row of the batch: its prefix parts and its own.  With MANY rows a warp
+// each, which hide each other's trips to memory (64 registers, more warps);
+// with few a block each.
 template <bool FP16, bool MANY>
-__global__ void __launch_bounds__(32 * kJoinWarps, MANY ? 8 : 4) k_paged_join(const __grid_constant__ JoinArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps, 8) k_paged_join(const __grid_constant__ JoinArgs a) {
+  __shared__ JoinShared sh;
   const PagedGeom& g = a.g;
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = MANY ? blockIdx.x * kJoinWarps + warp : blockIdx.x;
   const int t = row / g.Hq, h = row - t * g.Hq;
   wait_for_previous();
   if (t >= g.Tq) return;
   const int ntok = batch_tokens(g);
   const int kvh = h / g.G, hh = h - kvh * g.G;
   int4 own = a.meta[(int64_t)t * g.Hkv + kvh];
-  const int64_t PU = a.prefix.head->units;
-  const int workers = max(1, min((int)a.prefix.head->workers, a.prefix.n));
+  const int64_t PU = a.direct ? 0 : a.prefix.head->units;
+  const int64_t PW = a.direct ? 0 : a.prefix.head->workers;
   if (t >= ntok) return;
   own.x = max(0, min(own.x, a.own.n - 1));  // rows of a refused sequence were never written
   own.y = max(own.x, min(own.y, a.own.n - 1));
   own.z = max(0, min(own.z, a.own.c.tpt - 1));
-  const PagedCut& c = a.prefix.c;
-  const int npt = (ntok + c.tpt - 1) / c.tpt, rt = t / c.tpt;
-  const int64_t np = ((int64_t)g.prefix + (1 << c.kt_log2) - 1) >> c.kt_log2;
-  const int team = team_size(c, npt, workers), n = shares_of(PU, workers / team);
-  const int64_t u0 = (team > 1 ? (int64_t)kvh : (int64_t)kvh * npt + rt) * np;
-  const int c0 = share_owner(PU, n, u0), c1 = share_owner(PU, n, u0 + np - 1);
-  const int parts = c1 - c0 + 1, member = team > 1 ? rt : 0, prow = (t - rt * c.tpt) * g.G + hh;
-  RowSum s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-  add_parts<MANY>(s, parts + own.y - own.x + 1, lane, [&](int j, const float*& acc) {
+  int parts = 0, c0 = 0, team = 1, member = 0, prow = 0;
+  if (!a.direct) {
+    const PagedCut& c = a.prefix.c;
+    const int npt = (ntok + c.tpt - 1) / c.tpt, rt = t / c.tpt;
+    const int64_t np = ((int64_t)g.prefix + (1 << c.kt_log2) - 1) >> c.kt_log2;
+    const int workers = max(1, min((int)PW, a.prefix.n));
+    team = team_size(c, npt, workers);
+    const int n = shares_of(PU, workers / team);
+    const int64_t u0 = (team > 1 ? (int64_t)kvh : (int64_t)kvh * npt + rt) * np;
+    c0 = share_owner(PU, n, u0);
+    parts = share_owner(PU, n, u0 + np - 1) - c0 + 1;
+    member = team > 1 ? rt : 0;
+    prow = (t - rt * c.tpt) * g.G + hh;
+  } else if (own.x == own.y) {
+    return;
+  }
+  auto part = [&](int j, const float*& acc) {
     if (j < parts)
       return parts == 1 ? dense_part(a.prefix.part, 0, row, acc)
                         : split_part(a.prefix.part, c0, j, team, member, prow, acc);
     return own.x == own.y ? dense_part(a.own.part, 1, row, acc)
                           : split_part(a.own.part, own.x, j - parts, 1, 0, own.z * g.G + hh, acc);
-  });
-  finish_row<FP16>(a, s, row, lane);
+  };
+  const int cnt = parts + own.y - own.x + 1;
+  RowSum s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  if constexpr (MANY) add_parts<4>(s, cnt, lane, part);
+  else s = block_add_parts(sh, cnt, warp, lane, part);
+  if (MANY || warp == 0) finish_row<FP16>(a, s, row, lane);
 }
 
-// own items that two or more workers share (all others are the result already):
-// blocks (c, y) take the rows of the one that begins in share c and goes on
+// chunks: own items that two or more workers share (all others are the result
+// already); block (c, y) takes every gridDim.y-th four rows of the one that
+// begins in share c and goes on, a warp each
 template <bool FP16>
 __global__ void __launch_bounds__(32 * kJoinWarps) k_paged_join_split(const __grid_constant__ JoinArgs a) {
   const PagedGeom& g = a.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   wait_for_previous();
   const SplitItem it = a.split[blockIdx.x];
-  const int lane = threadIdx.x & 31;
-  for (int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); r < it.ntok * g.G; r += gridDim.y * kJoinWarps) {
+  for (int r = blockIdx.y * kJoinWarps + warp; r < it.ntok * g.G; r += gridDim.y * kJoinWarps) {
     const int t = r / g.G;
     RowSum s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    add_parts<false>(s, it.c1 - (int)blockIdx.x + 1, lane,
-              [&](int j, const float*& acc) { return split_part(a.own.part, blockIdx.x, j, 1, 0, r, acc); });
+    add_parts<8>(s, it.c1 - (int)blockIdx.x + 1, lane,
+                 [&](int j, const float*& acc) { return split_part(a.own.part, blockIdx.x, j, 1, 0, r, acc); });
     finish_row<FP16>(a, s, (size_t)(it.tok0 + t) * g.Hq + it.kvh * g.G + (r - t * g.G), lane);
   }
 }

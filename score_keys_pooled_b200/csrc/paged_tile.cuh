@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
     }
     if (!ok && lane == 0) {
       set_error(kErrTimeout);
-      if (a.direct && is_k) a.split[blockIdx.x] = {0, 0, 0, 0};
+      if (a.split && is_k) a.split[blockIdx.x] = {0, 0, 0, 0};
     }
     // nothing may land in shared memory after the CTA ends
     for (uint32_t k = it > (uint32_t)nst ? it - nst : 0; k < it; ++k)
