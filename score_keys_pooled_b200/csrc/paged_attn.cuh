@@ -30,13 +30,15 @@
 //     with the 128-byte swizzle, read back by ldmatrix without bank conflicts.
 //   * P = 2^(s - m) is rounded to the cache's type for the second product (its
 //     matrix instruction has one input type); sums use the unrounded value.
-//     The reference m moves only when the maximum grows by more than 2^8.  In
-//     fp16 P is scaled by 2^7, so probabilities down to 2^-21 stay normal.
+//     The reference m is the maximum of a row's first keys and moves only when P
+//     would leave its type's range.  In fp16 P is scaled by 2^7, so
+//     probabilities down to 2^-21 stay normal.
 //   * keys behind a sequence's length: scores are replaced before they are
 //     used, V rows are zeroed in shared memory, so whatever the page holds
 //     there (NaN included) cannot reach the result.
 #pragma once
 #include <cuda.h>
+#include <limits.h>
 
 #include "paged_sched.cuh"
 
@@ -287,6 +289,9 @@ __global__ void __launch_bounds__(32 * kPgWarps, 1)
   // ---- the rows
   const int r0 = lane >> 2, cq = 2 * (lane & 3);
   constexpr float kShift = FP16 ? 7.f : 0.f;
+  // A row's reference is the maximum of the first keys it saw; it moves when P
+  // would leave the type's range (fp16: 2^15; bf16: far from fp32's end)
+  constexpr float kPgMove = FP16 ? 32768.f : 1.15e18f;
   uint32_t it = 0;
   for (uint32_t pi = 0; ok; ++pi) {
     if (!warp_ok(mbar_wait_bounded(full(it % C::kStages), (it / C::kStages) & 1))) { ok = false; break; }
@@ -304,7 +309,7 @@ __global__ void __launch_bounds__(32 * kPgWarps, 1)
       const int r = 16 * rt + r0 + 8 * k;
       has[k] = r < rows;
       const int tt = has[k] ? r / g.G : 0, h = has[k] ? r - tt * g.G : 0;
-      lim_own[k] = has[k] ? p.off + tt + 1 : 0;
+      lim_own[k] = has[k] ? p.off + tt + 1 : INT_MAX;  // rows of nobody see everything: no masks for their sake
       orow[k] = (size_t)(p.tok0 + tt) * g.Hq + p.kvh * g.G + h;
       const uint16_t* q = a.Q + orow[k] * kD + cq;
 #pragma unroll
@@ -318,11 +323,14 @@ __global__ void __launch_bounds__(32 * kPgWarps, 1)
     for (int n = 0; n < 16; ++n)
 #pragma unroll
       for (int k = 0; k < 4; ++k) acc[n][k] = 0.f;
-    float ref[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+    float ref[2] = {0.f, 0.f}, sum[2] = {0.f, 0.f};
+    bool fresh = true;  // the references are still to be set
 
     for (int keys = 0; keys < 2; ++keys) {
     const KeyRun r = key_run(g, p, keys);
-    const int lim[2] = {keys == 0 ? (has[0] ? r.len : 0) : lim_own[0], keys == 0 ? (has[1] ? r.len : 0) : lim_own[1]};
+    const int lim[2] = {keys == 0 ? r.len : lim_own[0], keys == 0 ? r.len : lim_own[1]};
+    // the fewest keys that a row of the warp sees
+    const int lim_min = __reduce_min_sync(0xffffffffu, min(lim[0], lim[1]));
     for (int t = r.sub0; t < r.sub1; ++t, ++it) {
       const int st = it % C::kStages;
       if (!warp_ok(mbar_wait_bounded(full(st), (it / C::kStages) & 1))) { ok = false; break; }
@@ -343,49 +351,61 @@ __global__ void __launch_bounds__(32 * kPgWarps, 1)
             mma16816<FP16>(y[1], qf[kk + 1], c[2], c[3]);
           }
         }
-        // hidden keys, the rows' maxima
-        float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int key = key0 + 8 * n + cq + (k & 1);
-            x[n][k] = key < lim[k >> 1] ? (x[n][k] + y[n][k]) * kPgScale : -INFINITY;
-            mx[k >> 1] = fmaxf(mx[k >> 1], x[n][k]);
-          }
-        bool move = false;
+          for (int k = 0; k < 4; ++k) x[n][k] += y[n][k];
+        if (key0 + kPgSub > lim_min) {  // hidden keys
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
-          mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
-          move |= mx[k] - kShift > ref[k] + 8.f;
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (key0 + 8 * n + cq + (k & 1) >= lim[k >> 1]) x[n][k] = -INFINITY;
         }
-        if (__any_sync(0xffffffffu, move)) {
+        float px[2][4];
+        auto exponentials = [&]() {
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) px[n][k] = ex2_approx(fmaf(x[n][k], kPgScale, -ref[k >> 1]));
+        };
+        bool move = fresh;
+        if (!fresh) {
+          exponentials();
+          const float top = fmaxf(fmaxf(fmaxf(px[0][0], px[0][1]), fmaxf(px[0][2], px[0][3])),
+                                  fmaxf(fmaxf(px[1][0], px[1][1]), fmaxf(px[1][2], px[1][3])));
+          move = __any_sync(0xffffffffu, top > kPgMove);
+        }
+        if (move) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            if (!(mx[k] - kShift > ref[k] + 8.f)) continue;
-            const float f = ex2_approx(ref[k] - (mx[k] - kShift));  // ref -inf: 0
-            ref[k] = mx[k] - kShift;
-            sum[k] *= f;
+            float mx = fmaxf(fmaxf(x[0][2 * k], x[0][2 * k + 1]), fmaxf(x[1][2 * k], x[1][2 * k + 1]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            mx = fmaf(mx, kPgScale, -kShift);
+            if (fresh) {
+              ref[k] = mx == -INFINITY ? 0.f : mx;  // sees nothing here, and nothing behind it
+            } else if (mx > ref[k]) {
+              const float f = ex2_approx(ref[k] - mx);
+              ref[k] = mx;
+              sum[k] *= f;
 #pragma unroll
-            for (int n = 0; n < 16; ++n) {
-              acc[n][2 * k] *= f;
-              acc[n][2 * k + 1] *= f;
+              for (int n = 0; n < 16; ++n) {
+                acc[n][2 * k] *= f;
+                acc[n][2 * k + 1] *= f;
+              }
             }
           }
+          fresh = false;
+          exponentials();
         }
         uint32_t pf[4];
-        {
-          const float m0 = ref[0] == -INFINITY ? 0.f : ref[0], m1 = ref[1] == -INFINITY ? 0.f : ref[1];
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const float p0 = ex2_approx(x[n][0] - m0), p1 = ex2_approx(x[n][1] - m0);
-            const float p2 = ex2_approx(x[n][2] - m1), p3 = ex2_approx(x[n][3] - m1);
-            sum[0] += p0 + p1;
-            sum[1] += p2 + p3;
-            pf[2 * n] = pack2<FP16>(p0, p1);
-            pf[2 * n + 1] = pack2<FP16>(p2, p3);
-          }
+        for (int n = 0; n < 2; ++n) {
+          sum[0] += px[n][0] + px[n][1];
+          sum[1] += px[n][2] + px[n][3];
+          pf[2 * n] = pack2<FP16>(px[n][0], px[n][1]);
+          pf[2 * n + 1] = pack2<FP16>(px[n][2], px[n][3]);
         }
         if (key0 + kPgSub > r.len) {
           // V rows behind the list: zero (the stream's other warps write the
@@ -427,6 +447,7 @@ __global__ void __launch_bounds__(32 * kPgWarps, 1)
     for (int k = 0; k < 2; ++k) {
       sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 1);
       sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 2);
+      if (sum[k] == 0.f) ref[k] = -INFINITY;  // saw no key
     }
     const bool whole = p.first && p.last;
 #pragma unroll
