@@ -34,6 +34,11 @@ bool take_view(const s2o_view* v, RowView* out) {
   return true;
 }
 
+// an output whose rows fall on one another
+bool overlaps(const RowView& v, int64_t B, int64_t N, int64_t H) {
+  return (B > 1 && v.sb == 0) || (N > 1 && v.st == 0) || (H > 1 && v.sh == 0);
+}
+
 s2o_status check_cache(const s2o_cache_config* c) {
   if (!c) return S2O_ERR_INVALID_ARG;
   if (c->Hq <= 0 || c->Hkv <= 0 || c->d <= 0 || c->page_size <= 0 || c->num_pages <= 0 || c->nseq <= 0 ||
@@ -227,6 +232,7 @@ s2o_status s2o_rotary(const s2o_rotary_config* rotary, int32_t dtype, int32_t B,
   std::memset(&a.q, 0, 4 * sizeof(RowView));
   if (Hq && (!take_view(q, &a.q) || !take_view(q_out, &a.qo))) return S2O_ERR_INVALID_ARG;
   if (Hkv && (!take_view(k, &a.k) || !take_view(k_out, &a.ko))) return S2O_ERR_INVALID_ARG;
+  if ((Hq && overlaps(a.qo, B, N, Hq)) || (Hkv && overlaps(a.ko, B, N, Hkv))) return S2O_ERR_INVALID_ARG;
   a.pos = positions;
   a.B = B; a.N = N; a.Hq = Hq; a.Hkv = Hkv;
   const int64_t total = (int64_t)B * N;
@@ -257,7 +263,8 @@ s2o_status s2o_cache_append(const s2o_cache_config* cfg, const s2o_rotary_config
   std::memset(&a.q, 0, 4 * sizeof(RowView));
   if (cfg->Tq == 0) return S2O_OK;
   if (!take_view(k, &a.k) || !take_view(v, &a.v)) return S2O_ERR_INVALID_ARG;
-  if (q && (!take_view(q, &a.q) || !take_view(q_out, &a.qo))) return S2O_ERR_INVALID_ARG;
+  if (q && (!take_view(q, &a.q) || !take_view(q_out, &a.qo) || overlaps(a.qo, 1, cfg->Tq, cfg->Hq)))
+    return S2O_ERR_INVALID_ARG;
   if ((int64_t)cfg->Hq + 2 * (int64_t)cfg->Hkv > 4096) return S2O_ERR_UNSUPPORTED_SHAPE;
   a.pos = positions;
   a.table = page_table; a.q_start = q_start; a.kv_len = kv_len;

@@ -31,8 +31,8 @@
 //   * P = 2^(s - m) is rounded to the cache's type for the second product (its
 //     matrix instruction has one input type); sums use the unrounded value.
 //     The reference m is the maximum of a row's first keys and moves only when P
-//     would leave its type's range.  In fp16 P is scaled by 2^7, so
-//     probabilities down to 2^-21 stay normal.
+//     passes 2^15.  In fp16 P is scaled by 2^7, so probabilities down to 2^-21
+//     stay normal.
 //   * keys behind a sequence's length: scores are replaced before they are
 //     used, V rows are zeroed in shared memory, so whatever the page holds
 //     there (NaN included) cannot reach the result.
@@ -49,6 +49,11 @@ constexpr int kPgSub = 16;                         // keys of a stage
 constexpr uint32_t kPgStage = 2 * kPgSub * 256;    // K then V, each two halves of 16 rows x 128 bytes
 constexpr int kPgWarps = 8;
 constexpr float kPgScale = 1.4426950408889634f * 0.08838834764831845f;  // log2(e) / sqrt(128)
+// A row's reference is the maximum of the first keys it saw.  Later ones need
+// no maximum: numbers with an exponent lose nothing by being large, so the
+// reference moves only when P passes 2^15: in fp16 the type's end, in bf16 room
+// enough for the accumulator below fp32's.
+constexpr float kPgMove = 32768.f;
 
 template <int R>
 struct PgDecode {
@@ -289,9 +294,6 @@ __global__ void __launch_bounds__(32 * kPgWarps, 1)
   // ---- the rows
   const int r0 = lane >> 2, cq = 2 * (lane & 3);
   constexpr float kShift = FP16 ? 7.f : 0.f;
-  // A row's reference is the maximum of the first keys it saw; it moves when P
-  // would leave the type's range (fp16: 2^15; bf16: far from fp32's end)
-  constexpr float kPgMove = FP16 ? 32768.f : 1.15e18f;
   uint32_t it = 0;
   for (uint32_t pi = 0; ok; ++pi) {
     if (!warp_ok(mbar_wait_bounded(full(it % C::kStages), (it / C::kStages) & 1))) { ok = false; break; }

@@ -370,12 +370,6 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
     // ------------------------------------------------------------------ softmax
     regs_increase<kRegsSoftmax>();
     constexpr float kShift = FP16 ? 7.f : 0.f;
-    // A row's reference is the maximum of the first keys it saw.  Later ones
-    // need no maximum: numbers with an exponent lose nothing by being large,
-    // so the reference moves only when a chunk's sum says that P may leave its
-    // type's range (fp16: 2^15; bf16: far from fp32's end, which O and the sum
-    // must keep clear of)
-    constexpr float kPtMove = FP16 ? 32768.f : 1.15e18f;
     const int qi = warp >> 2;
     const int r = tid & 127;
     const int rt = r / g.G, rh = r - rt * g.G;  // token of the tile, head of the group
@@ -458,9 +452,9 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
           if (m_run == -INFINITY) m_run = mt;
         }
         exponentials();
-        if (__any_sync(0xffffffffu, rs > kPtMove)) {
+        if (__any_sync(0xffffffffu, rs > kPgMove)) {
           const float mt = reference();
-          const bool move = rs > kPtMove;
+          const bool move = rs > kPgMove;
           const float alpha = move ? ex2_approx(m_run - mt) : 1.f;
           if (move) m_run = mt;
           ell *= alpha;

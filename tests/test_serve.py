@@ -330,6 +330,74 @@ def test_a_rising_and_a_falling_run_of_scores():
         b.check(O, lse, sign)
 
 
+def dense_reference(b, q, k, v, table, kv_len, prefix_pages):
+    """SO.attend for batches too large for it: the same in fp64 with torch on the
+    GPU, a sequence at a time."""
+    Tq, Hq, Hkv, d = q.shape[0], q.shape[1], k.shape[1], 128
+    G, P = Hq // Hkv, b.P
+    rows = lambda c, pages, n: c[pages.long()].transpose(1, 2).reshape(-1, Hkv, d)[:n].double()
+    O, A = (torch.zeros(Tq, Hq, d, dtype=torch.float64, device="cuda") for _ in range(2))
+    lse, S = (torch.zeros(Tq, Hq, dtype=torch.float64, device="cuda") for _ in range(2))
+    n = torch.zeros(Tq, dtype=torch.int64)
+    pk, pv = rows(k, prefix_pages, P), rows(v, prefix_pages, P)
+    t0 = 0
+    for s, (m, L) in enumerate(zip(b.new, b.len)):
+        if m:
+            used = table[s, :-(-L // b.page)]
+            kk = torch.cat([pk, rows(k, used, L)]).permute(1, 2, 0)                  # [Hkv, d, n]
+            vv = torch.cat([pv, rows(v, used, L)]).transpose(0, 1)                   # [Hkv, n, d]
+            qq = q[t0:t0 + m].double().view(m, Hkv, G, d).permute(1, 2, 0, 3).reshape(Hkv, G * m, d)
+            x = (qq @ kk).view(Hkv, G, m, -1) / d ** 0.5
+            key = torch.arange(P + L, device="cuda")
+            at = P + L - m + torch.arange(m, device="cuda")
+            hidden = key[None] > at[:, None]
+            x = x.masked_fill(hidden, float("-inf")).view(Hkv, G * m, -1)
+            p = torch.softmax(x, -1)
+            back = lambda y: y.view(Hkv, G, m, -1).permute(2, 0, 1, 3).reshape(m, Hq, -1)
+            O[t0:t0 + m], A[t0:t0 + m] = back(p @ vv), back(p @ vv.abs())
+            lse[t0:t0 + m] = back(torch.logsumexp(x, -1)[..., None])[..., 0]
+            S[t0:t0 + m] = back((qq.abs() @ kk.abs()).amax(-1, keepdim=True))[..., 0] / d ** 0.5
+            n[t0:t0 + m] = (at + 1).cpu()
+        t0 += m
+    return f64(O), f64(lse), f64(A), f64(S), n.numpy()
+
+
+# shapes that reach every way the kernels are put together: (new, own keys, prefix, page, Hq, Hkv, launches)
+WAYS = {
+    "decode_walks_prefix": ([1] * 40, [1 + 7 * i % 300 for i in range(40)], 40, 16, 32, 8, 2),
+    "decode_two_row_tiles": ([3, 8, 5] * 5, [20, 8, 400] * 5, 0, 32, 16, 4, 2),
+    "prefix_items_beside_own": ([1] * 24, [1 + 11 * i % 200 for i in range(24)], 1500, 64, 8, 2, 2),
+    "tiles_in_teams": ([1] * 200, [1 + i % 90 for i in range(200)], 4100, 64, 32, 8, 3),
+    "tiles_in_teams_ragged": ([2, 0, 4, 1] * 60, [70, 3, 4, 31] * 60, 9001, 128, 8, 2, 3),
+    "tiles_without_teams": ([1] * 700, [1 + i % 40 for i in range(700)], 3000, 16, 32, 1, 3),
+    "tiles_of_128_rows": ([1] * 30, [1 + i % 60 for i in range(30)], 30000, 32, 8, 2, 3),
+    "chunks_walk_prefix": ([100, 33, 260], [100, 400, 900], 700, 32, 8, 2, 2),
+    "chunks_prefix_items": ([9] * 64, [9 + 5 * i for i in range(64)], 6000, 16, 32, 8, 2),
+    "chunks_alone_long": ([1500], [2600], 0, 128, 4, 1, 2),
+    "chunk_groups_of_48": ([1, 2, 9], [100, 2, 300], 500, 64, 48, 1, 2),
+}
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp16"])
+@pytest.mark.parametrize("way", list(WAYS))
+def test_every_way_of_the_attention(way, t):
+    new, length, P, page, Hq, Hkv, launches = WAYS[way]
+    b = Batch(new, length, P, page, Hq, Hkv, TYPES[t], seed=11, extra_rows=1)
+    q, k, v, table, qs, kl, pre = b.dev()
+    ws = s2o.alloc_attention_paged(b.cfg).fill_(255)
+    O, lse = s2o.attention_paged(b.cfg, q, k, v, table, qs, kl, prefix_pages=pre, workspace=ws)
+    assert s2o.last_launch_count() == launches
+    assert s2o.last_device_error() == 0
+    b.want = dense_reference(b, q, k, v, table, kl, pre)
+    b.check(O, lse, way)
+    # called again and again, other work of the same kernels in between: the same bits
+    c = Batch([1, 40], [77, 90], 300, 16, 8, 2, TYPES[t], seed=12)
+    for _ in range(10):
+        O2, lse2 = s2o.attention_paged(b.cfg, q, k, v, table, qs, kl, prefix_pages=pre, workspace=ws)
+        attend(c)
+        assert torch.equal(O2[:b.own], O[:b.own]) and torch.equal(lse2[:b.own], lse[:b.own])
+
+
 def test_lse_may_be_left_out_and_the_workspace_must_fit():
     b = Batch([1, 1], [30, 9], 40)
     q, k, v, table, qs, kl, pre = b.dev()

@@ -142,6 +142,8 @@ def test_rotary_refusals(L):
         assert L.s2o_rotary(*(good[:i] + [value] + good[i + 1:])) == 1, i
     for i in (6, 7, 9, 10):
         assert L.s2o_rotary(*(good[:i] + [view(b=12)] + good[i + 1:])) == 1, i
+    for i in (9, 10):  # an output whose rows fall on one another; an input may be broadcast
+        assert L.s2o_rotary(*(good[:i] + [view(t=0)] + good[i + 1:])) == 1, i
     assert L.s2o_rotary(*(good[:4] + [5000] + good[5:])) == 2
     assert L.s2o_rotary(*(good[:3] + [0] + good[4:])) == 0  # nothing to turn
     assert s2o.last_launch_count() == 0
