@@ -105,7 +105,7 @@ PagedPlan paged_plan(const s2o_cache_config* c, int sms) {
   const double units = c->Hkv * std::ceil(prefix / (1 << own.kt_log2)) / sms;
   const double unit = p.chunks ? (2 * c->max_q <= p.tile.tpt ? 1.3 : 2.25) : (p.R == 1 ? 0.6 : 0.9);
   const double join = 5 + 1.5e-3 * tokens * c->Hq;
-  const double walk = units * unit * (seqs + std::floor(tokens / own.tpt));
+  const double walk = units * unit * (seqs + std::floor((tokens - seqs) / own.tpt));
   const double items = units * (p.chunks ? 2.25 : unit) * std::ceil(tokens / own.tpt) + join;
   const double tiles = p.chunks ? INFINITY
                                 : c->Hkv * std::ceil(prefix / 128) / sms * std::ceil(tokens / p.tile.tpt) * 2.25 + join + 10;

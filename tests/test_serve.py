@@ -366,7 +366,7 @@ def dense_reference(b, q, k, v, table, kv_len, prefix_pages):
 WAYS = {
     "decode_walks_prefix": ([1] * 40, [1 + 7 * i % 300 for i in range(40)], 40, 16, 32, 8, 2),
     "decode_two_row_tiles": ([3, 8, 5] * 5, [20, 8, 400] * 5, 0, 32, 16, 4, 2),
-    "prefix_items_beside_own": ([1] * 24, [1 + 11 * i % 200 for i in range(24)], 1500, 64, 8, 2, 2),
+    "decode_prefix_items": ([1] * 24, [1 + 11 * i % 200 for i in range(24)], 5000, 64, 8, 2, 2),
     "tiles_in_teams": ([1] * 200, [1 + i % 90 for i in range(200)], 4100, 64, 32, 8, 3),
     "tiles_in_teams_ragged": ([2, 0, 4, 1] * 60, [70, 3, 4, 31] * 60, 9001, 128, 8, 2, 3),
     "tiles_without_teams": ([1] * 700, [1 + i % 40 for i in range(700)], 3000, 16, 32, 1, 3),
