@@ -140,6 +140,10 @@ __device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* m
 // are seen (both nothing when the launch did not ask for it).
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+// the tensor map on its way before the first copy asks for it
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 // two neighbouring values of a finished row
 template <bool FP16>
 __device__ __forceinline__ void store2(void* O, int out_f32, size_t at, float x, float y) {
@@ -215,15 +219,19 @@ __global__ void __launch_bounds__(32 * kPgWarps, 1)
   const PagedGeom& g = a.g;
   let_next_start();
 
+  if (tid == 0) {
+    prefetch_map(&tmK);
+    prefetch_map(&tmV);
+  }
   if (rt == 0 && lane < C::kStages) {
     mbar_init(full(lane), 1);
     mbar_init(empty(lane), R);
     fence_mbar_init();
   }
-  const OwnRun run = own_run(g, a.c, reinterpret_cast<int64_t*>(sgen + C::kOffRed));
+  SchedFound* found = reinterpret_cast<SchedFound*>(sgen + C::kOffRed + 34 * 8);
+  const OwnRun run = own_run(g, a.c, C::kStreams, reinterpret_cast<int64_t*>(sgen + C::kOffRed), found);
   const int ctas = a.beside ? decode_sms(g, a.other, batch_tokens(g), run.total, a.own_ns, gridDim.x) : (int)gridDim.x;
-  Sched sc = sched_begin(g, a.c, C::kStreams, stream, ctas, run,
-                         reinterpret_cast<SchedFound*>(sgen + C::kOffRed + 34 * 8));
+  Sched sc = sched_begin(g, a.c, C::kStreams, stream, ctas, run, found);
   if (tid == 0 && blockIdx.x == 0) *a.head = {sc.U, ctas * C::kStreams};
   __syncthreads();
 

@@ -192,12 +192,14 @@ struct SchedFound {
 };
 // Units of all own items, and where this thread's run of sequences [s0, s1)
 // stands among them.  Block-wide, blockDim.x a multiple of 32 up to 1024;
-// `red` is 33 words of shared memory, free again after the next barrier.
+// `red` is a word of shared memory for each warp; `found` (`own` entries) is
+// made ready for sched_begin on the way.
 struct OwnRun {
   int s0, s1;
   int64_t begin, mine, total;
 };
-__device__ __forceinline__ OwnRun own_run(const PagedGeom& g, const PagedCut& c, int64_t* red) {
+__device__ __forceinline__ OwnRun own_run(const PagedGeom& g, const PagedCut& c, int own, int64_t* red,
+                                          SchedFound* found) {
   const int tid = threadIdx.x, nth = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nth >> 5;
   const int per = (g.nseq + nth - 1) / nth;
   OwnRun r;
@@ -218,13 +220,13 @@ __device__ __forceinline__ OwnRun own_run(const PagedGeom& g, const PagedCut& c,
     if (lane >= o) incl += y;
   }
   if (lane == 31) red[warp] = incl;
+  if (tid < own) found[tid].seq = g.nseq;
   __syncthreads();
-  // every warp adds up the sums of the warps before it
-  int64_t v = lane < nw ? red[lane] : 0, before = lane < warp ? v : 0;
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) {
-    v += __shfl_xor_sync(0xffffffffu, v, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
+  // every thread adds up the sums of the warps before its own
+  int64_t v = 0, before = 0;
+  for (int w = 0; w < nw; ++w) {
+    if (w == warp) before = v;
+    v += red[w];
   }
   r.total = v;
   r.begin = before + incl - r.mine;
@@ -252,11 +254,9 @@ __device__ __forceinline__ int decode_sms(const PagedGeom& g, const PagedCut& ti
 // Total units and the item of the first unit of this thread's share.  A block
 // is `own` workers (1 to 8), `ctas` of the grid's blocks work: worker w of
 // block b is number w * ctas + b; the calling thread asks for worker `which`
-// of its block.  `run`: own_run() of the block (without own items: unused).
-// `found` (`own` entries) is in shared memory.  Block-wide.
+// of its block.  `run`, `found`: own_run()'s.  Block-wide.
 __device__ __forceinline__ Sched sched_begin(const PagedGeom& g, const PagedCut& c, int own, int which, int ctas,
                                              const OwnRun& run, SchedFound* found) {
-  const int tid = threadIdx.x;
   Sched s;
   const int workers = ctas * own, number = which * ctas + blockIdx.x;
   const bool works = blockIdx.x < ctas;
@@ -280,8 +280,6 @@ __device__ __forceinline__ Sched sched_begin(const PagedGeom& g, const PagedCut&
     return s;
   }
   const int64_t PU = (int64_t)s.npt * g.Hkv * np;
-  if (tid < own) found[tid].seq = g.nseq;
-  __syncthreads();
   s.U = PU + (c.own_items ? run.total : 0);
   s.n = shares_of(s.U, workers);
   s.me = number;

@@ -134,8 +134,14 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
   const int trows = tpt * g.G;    // its rows
 
   let_next_start();
+  if (tid == 0) {
+    prefetch_map(&tmQ);
+    prefetch_map(&tmK);
+    prefetch_map(&tmV);
+  }
   // side by side with the decode kernel: its items decide how many SMs are left
-  const OwnRun run = own_run(g, a.beside ? a.other : a.c, reinterpret_cast<int64_t*>(sgen + kPtOffRed));
+  SchedFound* found = reinterpret_cast<SchedFound*>(sgen + kPtOffRed + 34 * 8);
+  const OwnRun run = own_run(g, a.beside ? a.other : a.c, 1, reinterpret_cast<int64_t*>(sgen + kPtOffRed), found);
   const int ctas =
       gridDim.x - (a.beside ? decode_sms(g, a.c, batch_tokens(g), run.total, a.own_ns, gridDim.x) : 0);
   if (blockIdx.x >= ctas) return;  // an SM for the decode kernel
@@ -158,7 +164,7 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
     tmem_alloc(smem_u32((const void*)tmem_slot), kTmem2Cols);
     tmem_relinquish();
   }
-  Sched sc = sched_begin(g, a.c, 1, 0, ctas, run, reinterpret_cast<SchedFound*>(sgen + kPtOffRed + 34 * 8));
+  Sched sc = sched_begin(g, a.c, 1, 0, ctas, run, found);
   if (tid == 0 && blockIdx.x == 0) *a.head = {sc.U, ctas};
   tc_fence_before();
   __syncthreads();
