@@ -464,7 +464,8 @@ s2o_status s2o_cache_append(const s2o_cache_config* cfg, const s2o_rotary_config
  * cache: token i of a sequence's own keys sees the whole prefix and the own
  * keys 0 .. i.  The prefix is read once for the whole batch, each own key once.
  *   Q    device [Tq, Hq, 128], contiguous
- *   O    out, device [Tq, Hq, 128], in the cache's type (S2O_OUT_SAME) or fp32
+ *   O    out, device [Tq, Hq, 128], in the cache's type (S2O_OUT_SAME) or
+ *        fp32; not Q's memory
  *   lse  out, device fp32 [Tq, Hq]: log sum_j exp(s_ij); or NULL
  *   workspace  device scratch of s2o_attention_paged_workspace_size() bytes
  *        (on the device the call runs on), 256-byte aligned; contents need no
@@ -490,8 +491,8 @@ const char* s2o_status_string(s2o_status st);
  */
 s2o_status s2o_last_device_error(s2o_stream_t stream);
 
-/* Number of kernels the last s2o_plan / s2o_attention / s2o_plan_contiguous
- * call on this thread launched (the library's own kernels only). */
+/* Number of kernels the last s2o_plan / s2o_attention / s2o_plan_contiguous or
+ * serving call on this thread launched (the library's own kernels only). */
 int32_t s2o_last_launch_count(void);
 
 /*

@@ -417,6 +417,8 @@ def rotary(r: RotaryConfig, q, k, positions, q_out=None, k_out=None, inverse: bo
         _refuse(f"rotary: {t} is neither bfloat16 nor float16")
     Hq, qi, qo, q_out = _turned("rotary: q", q, q_out, B, N, t, dev, inverse, stream)
     Hkv, ki, ko, k_out = _turned("rotary: k", k, k_out, B, N, t, dev, inverse, stream)
+    if positions is None:
+        _refuse("rotary: positions")
     pos = _plain(positions, "rotary: positions", (r.naxes, B, N), torch.int32, dev)
     _call_on(dev, stream, lib().s2o_rotary, "s2o_rotary", r, FP16 if t is torch.float16 else BF16, B, N, Hq, Hkv, qi,
              ki, pos, qo, ko, int(inverse))

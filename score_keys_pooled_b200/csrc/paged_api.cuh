@@ -172,6 +172,7 @@ bool encode_query_map(CUtensorMap* map, const void* base, int Tq, int Hq, int G,
 }
 
 // launch that may start before the kernel in front of it is done
+// (an error is taken off the runtime's record: it is this call's to report)
 template <class... P, class... A>
 cudaError_t launch_early(void (*f)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s, bool early,
                          const A&... args) {
@@ -185,25 +186,31 @@ cudaError_t launch_early(void (*f)(P...), dim3 grid, unsigned threads, size_t sm
   cfg.stream = s;
   cfg.attrs = &at;
   cfg.numAttrs = early ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, f, args...);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, f, args...);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
+}
+
+template <class F>
+cudaError_t allow_smem(F f, size_t bytes) {
+  // the attribute belongs to the function on the current device; setting it
+  // again costs less than a microsecond
+  const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
 }
 
 template <bool FP16>
 cudaError_t launch_tile(const PagedArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, int n,
                         cudaStream_t s) {
-  cudaError_t e =
-      cudaFuncSetAttribute(k_paged_tile<FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPtSmem);
+  const cudaError_t e = allow_smem(k_paged_tile<FP16>, kPtSmem);
   if (e != cudaSuccess) return e;
-  k_paged_tile<FP16><<<n, kAttn2Threads, kPtSmem, s>>>(a, q, k, v);
-  return cudaGetLastError();
+  return launch_early(k_paged_tile<FP16>, n, kAttn2Threads, kPtSmem, s, false, a, q, k, v);
 }
 template <bool FP16, int R>
 cudaError_t launch_decode(const PagedArgs& a, const CUtensorMap& k, const CUtensorMap& v, int n, cudaStream_t s,
                           bool early) {
-  // the attribute belongs to the function on the current device; setting it
-  // again costs less than a microsecond
-  cudaError_t e = cudaFuncSetAttribute(k_paged_decode<FP16, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)PgDecode<R>::kSmem);
+  const cudaError_t e = allow_smem(k_paged_decode<FP16, R>, PgDecode<R>::kSmem);
   if (e != cudaSuccess) return e;
   return launch_early(k_paged_decode<FP16, R>, n, 32 * kPgWarps, PgDecode<R>::kSmem, s, early, a, k, v);
 }
@@ -257,11 +264,11 @@ s2o_status s2o_cache_append(const s2o_cache_config* cfg, const s2o_rotary_config
   AppendArgs a;
   st = rotary_table(rotary, false, &a.r);
   if (st != S2O_OK) return st;
+  if (cfg->Tq == 0) return S2O_OK;  // nothing to write; the tensors may have no memory
   if (!k || !v || !page_table || !q_start || !kv_len || !k_cache || !v_cache || !q != !q_out)
     return S2O_ERR_INVALID_ARG;
   if (!aligned16(k_cache) || !aligned16(v_cache)) return S2O_ERR_INVALID_ARG;
   std::memset(&a.q, 0, 4 * sizeof(RowView));
-  if (cfg->Tq == 0) return S2O_OK;
   if (!take_view(k, &a.k) || !take_view(v, &a.v)) return S2O_ERR_INVALID_ARG;
   if (q && (!take_view(q, &a.q) || !take_view(q_out, &a.qo) || overlaps(a.qo, 1, cfg->Tq, cfg->Hq)))
     return S2O_ERR_INVALID_ARG;
@@ -297,18 +304,18 @@ s2o_status s2o_attention_paged(const s2o_cache_config* cfg, const uint16_t* Q, c
   t_launches = 0;
   s2o_status st = check_cache(cfg);
   if (st != S2O_OK) return st;
+  if (cfg->Tq == 0) return S2O_OK;  // no rows; the tensors may have no memory
   if (!Q || !k_cache || !v_cache || !page_table || !q_start || !kv_len || !O || !workspace ||
       (cfg->prefix_len > 0 && !prefix_pages))
     return S2O_ERR_INVALID_ARG;
   if (out_dtype != S2O_OUT_SAME && out_dtype != S2O_OUT_F32) return S2O_ERR_INVALID_ARG;
-  if (!aligned16(Q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(O) ||
+  if (!aligned16(Q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(O) || O == Q ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return S2O_ERR_INVALID_ARG;
   const int n = sm_count();
   const PagedPlan p = paged_plan(cfg, n);
   const PagedWs w = paged_layout(cfg, p, n, workspace);
   if (workspace_bytes < w.bytes) return S2O_ERR_WORKSPACE_TOO_SMALL;
-  if (cfg->Tq == 0) return S2O_OK;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   PagedArgs a{};
   PagedGeom& g = a.g;
@@ -369,7 +376,7 @@ s2o_status s2o_attention_paged(const s2o_cache_config* cfg, const uint16_t* Q, c
   }
   if (e != cudaSuccess) return S2O_ERR_CUDA;
   ++t_launches;
-  return launch_status();
+  return S2O_OK;
 }
 
 }  // extern "C"

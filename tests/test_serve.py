@@ -398,6 +398,28 @@ def test_every_way_of_the_attention(way, t):
         assert torch.equal(O2[:b.own], O[:b.own]) and torch.equal(lse2[:b.own], lse[:b.own])
 
 
+def test_a_batch_without_tokens():
+    """No token at all, or rows that belong to nobody: nothing is written."""
+    b = Batch([0, 0], [30, 0], 40)
+    x = torch.zeros(0, 8, 128, device="cuda").bfloat16()
+    q, k, v, table, qs, kl, pre = b.dev()
+    O, lse = s2o.attention_paged(b.cfg, q, k, v, table, qs, kl, prefix_pages=pre)
+    assert O.shape == (0, 8, 128) and s2o.last_launch_count() == 0
+    s2o.cache_append(b.cfg, x, x[:, :2], x[:, :2], k, v, table, qs, kl, rotary=s2o.make_rotary())
+    assert s2o.last_launch_count() == 0
+    assert s2o.rotary(s2o.make_rotary(), x[None], None, torch.zeros(1, 1, 0, device="cuda", dtype=torch.int32))[0].numel() == 0
+    for P in (0, 40, 5000):
+        b = Batch([0, 0], [30, 0], P, extra_rows=70)
+        O = torch.full((70, 8, 128), 5.0, device="cuda", dtype=torch.bfloat16)
+        attend(b, O=O)
+        assert bool((O == 5.0).all())
+        q, k, v, table, qs, kl, pre = b.dev()
+        before = k.view(torch.int16).clone()
+        y = torch.ones(70, 2, 128, device="cuda").bfloat16()
+        s2o.cache_append(b.cfg, None, y, y, k, v, table, qs, kl)
+        assert torch.equal(k.view(torch.int16), before) and s2o.last_device_error() == 0
+
+
 def test_lse_may_be_left_out_and_the_workspace_must_fit():
     b = Batch([1, 1], [30, 9], 40)
     q, k, v, table, qs, kl, pre = b.dev()

@@ -96,12 +96,13 @@ def test_cache_config_validation(L, change, code):
 def test_attention_paged_refusals(L):
     c = cache()
     need = s2o.attention_paged_workspace_size(c)
-    good = [c, GOOD, GOOD, GOOD, GOOD, GOOD, GOOD, GOOD, GOOD, 0, None, GOOD, need, None]
+    good = [c, GOOD, GOOD, GOOD, GOOD, GOOD, GOOD, GOOD, ctypes.c_void_p(1 << 21), 0, None, GOOD, need, None]
     for i in (1, 2, 3, 4, 5, 6, 7, 8, 11):
         assert L.s2o_attention_paged(*(good[:i] + [None] + good[i + 1:])) == 1, i
     for i in (1, 2, 3, 8, 11):
         assert L.s2o_attention_paged(*(good[:i] + [ODD] + good[i + 1:])) == 1, i
     assert L.s2o_attention_paged(*(good[:9] + [2] + good[10:])) == 1
+    assert L.s2o_attention_paged(*(good[:8] + [ctypes.c_void_p(1 << 20)] + good[9:])) == 1  # O in Q's place
     assert L.s2o_attention_paged(*(good[:12] + [need - 1, None])) == 3
     assert L.s2o_attention_paged_workspace_size(c, None) == 1
     empty = cache(Tq=0)
@@ -176,7 +177,7 @@ def test_binding_refuses_tensors_the_call_was_not_made_for():
     x = torch.zeros(1, 3, 8, 128, dtype=torch.bfloat16)
     pos = torch.zeros(1, 1, 3, dtype=torch.int32)
     for change in (dict(q=x.float()), dict(q=x[0]), dict(k=x.half()), dict(k=x[:, :2]), dict(positions=pos[0]),
-                   dict(positions=pos.long()), dict(q=x.transpose(2, 3)), dict(q_out=x[:, :, :4]),
+                   dict(positions=pos.long()), dict(positions=None), dict(q=x.transpose(2, 3)), dict(q_out=x[:, :, :4]),
                    dict(q=None, k=None), dict()):
         a = dict(q=x, k=x, positions=pos)
         a.update(change)
