@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -54,6 +55,9 @@ class RotaryConfig(ctypes.Structure):
 class View(ctypes.Structure):
     _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_t", ctypes.c_int64),
                 ("stride_h", ctypes.c_int64)]
+
+
+_pack_view = struct.Struct("@Pqqq").pack  # a View's bytes
 
 
 class CacheConfig(ctypes.Structure):
@@ -130,7 +134,8 @@ def lib() -> ctypes.CDLL:
         L.s2o_last_stage_times.argtypes = [ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_char_p),
                                            ctypes.c_int32]
         L.s2o_last_stage_times.restype = ctypes.c_int32
-        _R, _V, _C = ctypes.POINTER(RotaryConfig), ctypes.POINTER(View), ctypes.POINTER(CacheConfig)
+        # views go in as packed bytes (a View made for each costs more than the rest of the call)
+        _R, _V, _C = ctypes.POINTER(RotaryConfig), _P, ctypes.POINTER(CacheConfig)
         i32 = ctypes.c_int32
         L.s2o_rotary.argtypes = [_R, i32, i32, i32, i32, i32, _V, _V, _P, _V, _V, i32, _P]
         L.s2o_cache_append.argtypes = [_C, _R, _V, _V, _V, _P, _P, _P, _P, _P, _P, _V, _P]
@@ -350,23 +355,23 @@ def _wrong(t, what, shape, dtype, device, layout):
 
 
 def _view3(t, what, shape, dtype, device):
-    """[T, H, 128] with contiguous rows."""
+    """[T, H, 128] with contiguous rows, as a packed s2o_view."""
     if t.dtype is not dtype or t.device != device or t.shape != shape:
         _wrong(t, what, shape, dtype, device, "contiguous rows")
     st, sh, one = t.stride()
     if one != 1 and t.numel():
         _wrong(t, what, shape, dtype, device, "contiguous rows")
-    return View(t.data_ptr(), 0, st, sh)
+    return _pack_view(t.data_ptr(), 0, st, sh)
 
 
 def _view4(t, what, shape, dtype, device):
-    """[B, N, H, 128] with contiguous rows."""
+    """[B, N, H, 128] with contiguous rows, as a packed s2o_view."""
     if t.dtype is not dtype or t.device != device or t.shape != shape:
         _wrong(t, what, shape, dtype, device, "contiguous rows")
     sb, st, sh, one = t.stride()
     if one != 1 and t.numel():
         _wrong(t, what, shape, dtype, device, "contiguous rows")
-    return View(t.data_ptr(), sb, st, sh)
+    return _pack_view(t.data_ptr(), sb, st, sh)
 
 
 def _plain(t, what, shape, dtype, device):
@@ -437,7 +442,7 @@ def _turned(name, src, dst, B, N, t, dev, inverse, stream):
     if dst is None:
         strides = (H * N * 128, H * 128, 128, 1) if inverse else (H * N * 128, 128, N * 128, 1)
         dst = _empty(shape, t, dev, stream, strides)
-        return H, vin, View(dst.data_ptr(), *strides[:3]), dst
+        return H, vin, _pack_view(dst.data_ptr(), *strides[:3]), dst
     return H, vin, _view4(dst, name + "_out", shape, t, dev), dst
 
 

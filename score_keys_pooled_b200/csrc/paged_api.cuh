@@ -5,7 +5,7 @@
 
 namespace {
 
-constexpr double kTwoPi = 6.283185307179586476925286766559;
+constexpr double kPerTurn = 0.15915494309189533576888376337251;  // 1 / (2 pi)
 
 s2o_status rotary_table(const s2o_rotary_config* r, bool inverse, RotaryTable* t) {
   std::memset(t, 0, sizeof(*t));
@@ -18,7 +18,7 @@ s2o_status rotary_table(const s2o_rotary_config* r, bool inverse, RotaryTable* t
   t->naxes = r->naxes;
   for (int i = 0; i < r->rot_dim / 2; ++i) {
     if (!std::isfinite(r->inv_freq[i]) || r->axis[i] >= r->naxes) return S2O_ERR_INVALID_ARG;
-    t->turns[i] = r->inv_freq[i] / kTwoPi;
+    t->turns[i] = r->inv_freq[i] * kPerTurn;
     t->axis[i] = r->axis[i];
   }
   return S2O_OK;

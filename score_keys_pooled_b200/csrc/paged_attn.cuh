@@ -1,6 +1,7 @@
-// Attention over a paged cache, few query rows a KV head: one token or a few
-// drafted ones of every sequence (the sequences' own keys), and a shared
-// prefix when the whole batch is few rows.
+// Attention over a paged cache, up to 32 query rows a sequence and KV head: one
+// token or a few drafted ones of every sequence against their own keys, and
+// against a shared prefix where the tile kernel (paged_tile.cuh) does not take
+// it.  The join of partial results, of either kernel, is at the end.
 //
 //   o_i = sum_j exp(s_ij) v_j / sum_j exp(s_ij),  s_ij = q_i . k_j / sqrt(d),
 //   j over the prefix and the own keys up to the row's own
@@ -13,18 +14,21 @@
 //     stream is a worker with a share of its own (paged_sched.cuh): it walks
 //     its keys 16 at a time through its own ring of 8 KB stages (192 KB of
 //     stages per SM), and its first warp issues the TMA boxes itself, each
-//     into the stage that the stream has just read.  A stream costs about 0.4
-//     us of latency per stage and some us per piece (sequence numbers, first
-//     loads, results); the other streams' reads go on meanwhile.  (One ring for
-//     the whole CTA, its 64-key stages cut into 16-key slices over four or
-//     eight warps with a join in shared memory at the end of each piece, spent
-//     8 to 13 us at every piece boundary: 58 and 79 us where this takes what
-//     is noted below.)
+//     into the stage that the stream has just read.  A stage costs a stream 0.7
+//     to 0.9 us of latency (two chains of products with the softmax between)
+//     and a piece some us (sequence numbers, first loads, results), while the
+//     other streams' reads go on: 16 sequences of up to 32K keys, 1.07 GB, take
+//     180 us, 6.0 TB/s, 91 % of the measured copy rate; even shares on SMs that
+//     are not equally near the memory (warps end between 128 and 173 us) are
+//     what is left.  One ring for the whole CTA, its 64-key stages cut into
+//     slices over four or eight warps and joined in shared memory at the end of
+//     each piece, spent 8 to 13 us at every piece boundary: 58 and 79 us on 64
+//     sequences of 512 keys where this takes 45.
 //   * a warp holds 16 query rows (an mma's M), their running reference and
-//     sum, and a 16 x 128 fp32 accumulator in registers; R = 2 or 4 warps of a
-//     stream hold further rows against the same stages.
+//     sum, and a 16 x 128 fp32 accumulator in registers; with R = 2 two warps
+//     of a stream hold 32 rows against the same stages.
 //   * products: mma.sync m16n8k16 (bf16 or fp16 in, fp32 out).  With at most
-//     64 rows a KV head the 128-row tcgen05 tile would be mostly empty and
+//     32 rows a KV head the 128-row tcgen05 tile would be mostly empty and
 //     its round trip through tensor memory sits on the latency of a step.
 //   * K and V stages are TMA boxes (64 columns x 16 rows, never across a page)
 //     with the 128-byte swizzle, read back by ldmatrix without bank conflicts.
@@ -499,8 +503,8 @@ __global__ void __launch_bounds__(32 * kPgWarps, 1)
 // own keys', each in share order, so the result does not depend on timing).  The
 // lanes take the (reference, sum) of up to 32 parts at once, agree on the
 // common reference and the weights, then read the accumulators with
-// independent loads: read one by one, each part costs a trip to L2 (23-29 us
-// for 20 parts a row instead of what is noted below).
+// independent loads: read one by one, each part costs a trip to L2 (23 to 29 us
+// for 2048 rows of 20 parts that take 9 so).
 
 struct JoinSide {
   PagedPart part;

@@ -10,9 +10,14 @@
 // split are those of k_sparse_attn2 (see there), with these differences:
 //   * S is double buffered, P written over the scores it came from (O and S fill
 //     the 512 columns), so that the products of the next half tile run during
-//     the softmax of this one; with one buffer a head the tensor core, the
-//     softmax and their hand-overs follow one another (1840 clocks a half tile
-//     of both heads, of which the products are about 1280);
+//     the softmax of this one: 256 sequences behind a 128K prefix, 598 us with
+//     one buffer, 582 with two.  A half tile of both heads takes about 1840
+//     clocks, of which the products are 1280 (64-key scores read Q again for
+//     half the work, 48 clocks a step where 32 would do) and the exponentials
+//     1024; one product of 128 keys (673 us: the heads fall into step and wait
+//     together), one issuer for both heads (594 and 679) and turns at the
+//     exponentials (596) were slower.  Repeated for long it is the power limit
+//     that holds it: 526 us a pass over 20 passes, 609 over 3000;
 //   * keys come from pages: warps 9 and 10 issue TMA boxes (64 columns x
 //     min(page, 64) rows, 128-byte swizzle) into the K and V rings; the last
 //     tile of a list that ends inside it has its missing V rows zeroed in

@@ -27,7 +27,7 @@ def cache(**kw):
 
 
 def view(ptr=1 << 20, b=0, t=1024, h=128):
-    return s2o.View(ptr, b, t, h)
+    return ctypes.byref(s2o.View(ptr, b, t, h))
 
 
 def test_oracle_rotation_is_complex_multiplication_and_inverts():
@@ -66,6 +66,11 @@ def test_oracle_attention_is_one_softmax_over_prefix_and_own_keys():
     p = np.exp(k @ q[1, 2] / np.sqrt(128))
     assert list(n) == [34, 35, 36] and np.allclose(lse[1, 2], np.log(p.sum()))
     assert np.allclose(O[1, 2], p @ v / p.sum())
+
+
+def test_a_packed_view_is_a_view():
+    v = s2o.View(1 << 40, 3, -8, 1 << 33)
+    assert bytes(v) == s2o._pack_view(1 << 40, 3, -8, 1 << 33)
 
 
 def test_rotary_config_checks():
