@@ -420,75 +420,64 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
           if (lane == 0) mbar_arrive(bar(kBarPFull + 2 * qi + (c & 1)));
           continue;
         }
-        float x[kBk];
-        tmem_ld32(tS, x);
-        tmem_ld32(tS + 32, x + 32);
-        tc_wait_ld();
-        const bool full = vis >= kBk;
-        // the largest score the row sees in this chunk, as a reference
-        auto reference = [&]() {
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        // (one copy each of the long unrolled parts: the code is fetched anew in
+        // every launch, through an L2 that the keys have passed through)
+        // the first keys a row sees set its reference; a chunk whose sum passes
+        // the limit moves it, and is done again from its scores
+        float x[kBk], rs = 0.f;  // scores, then P as pairs; its sum
+        bool set = __any_sync(0xffffffffu, m_run == -INFINITY);
+        for (int pass = 0; pass < 2; ++pass) {
+          tmem_ld32(tS, x);
+          tmem_ld32(tS + 32, x + 32);
+          tc_wait_ld();
+          if (vis < kBk) {
 #pragma unroll
-          for (int k = 0; k < kBk; ++k) m4[k & 3] = fmaxf(m4[k & 3], full || k < vis ? x[k] : -INFINITY);
-          return fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), kPgScale, -kShift);
-        };
-        float pw[kBk / 2], rs;  // P as pairs, their sum
-        auto exponentials = [&]() {
-          if (full) {
-            const uint64_t s2 = f2_pack(kPgScale, kPgScale), nm2 = f2_pack(-m_run, -m_run);
-            uint64_t rs2 = 0;
+            for (int k = 0; k < kBk; ++k)
+              if (k >= vis) x[k] = -INFINITY;
+          }
+          if (set) {
+            const bool move = m_run == -INFINITY || rs > kPgMove;
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int k = 0; k < kBk; k += 2) {
-              const uint64_t v = f2_fma(f2_pack(x[k], x[k + 1]), s2, nm2);
-              const float p0 = ex2_approx(f2_lo(v)), p1 = ex2_approx(f2_hi(v));
-              rs2 = f2_add(rs2, f2_pack(p0, p1));
-              pw[k / 2] = __uint_as_float(pack2<FP16>(p0, p1));
-            }
-            rs = f2_lo(rs2) + f2_hi(rs2);
-          } else {
-            rs = 0.f;
+            for (int k = 0; k < kBk; k += 2) m4[(k >> 1) & 3] = fmax3(m4[(k >> 1) & 3], x[k], x[k + 1]);
+            const float mt = fmaf(fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]), kPgScale, -kShift);
+            const float alpha = move && m_run != -INFINITY ? ex2_approx(m_run - mt) : 1.f;
+            if (move) m_run = mt;
+            ell *= alpha;
+            if (c > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+              if (!warp_wait(bar(kBarODone + 2 * qi + ((n - 1) & 1)), ((n - 1) >> 1) & 1, kSpinLimit)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+#pragma unroll 1
+              for (int cc = 0; cc < 128; cc += 32) {
+                float o[32];
+                tmem_ld32(tO + cc, o);
+                tc_wait_ld();
 #pragma unroll
-            for (int k = 0; k < kBk; k += 2) {
-              const float p0 = (k < vis) ? ex2_approx(fmaf(x[k], kPgScale, -m_run)) : 0.f;
-              const float p1 = (k + 1 < vis) ? ex2_approx(fmaf(x[k + 1], kPgScale, -m_run)) : 0.f;
-              rs += p0 + p1;
-              pw[k / 2] = __uint_as_float(pack2<FP16>(p0, p1));
+                for (int k = 0; k < 32; ++k) o[k] *= alpha;
+                tmem_st32(tO + cc, o);
+              }
             }
           }
-        };
-        // the first keys a row sees set its reference (nothing to rescale: its
-        // accumulator and sum are zero)
-        if (__any_sync(0xffffffffu, m_run == -INFINITY)) {
-          const float mt = reference();
-          if (m_run == -INFINITY) m_run = mt;
-        }
-        exponentials();
-        if (__any_sync(0xffffffffu, rs > kPgMove)) {
-          const float mt = reference();
-          const bool move = rs > kPgMove;
-          const float alpha = move ? ex2_approx(m_run - mt) : 1.f;
-          if (move) m_run = mt;
-          ell *= alpha;
-          if (c > 0) {
-            if (!warp_wait(bar(kBarODone + 2 * qi + ((n - 1) & 1)), ((n - 1) >> 1) & 1, kSpinLimit)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
+          const float m = m_run == -INFINITY ? 0.f : m_run;
+          const uint64_t s2 = f2_pack(kPgScale, kPgScale), nm2 = f2_pack(-m, -m);
+          uint64_t rs2 = 0;
 #pragma unroll
-            for (int cc = 0; cc < 128; cc += 32) {
-              float o[32];
-              tmem_ld32(tO + cc, o);
-              tc_wait_ld();
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] *= alpha;
-              tmem_st32(tO + cc, o);
-            }
+          for (int k = 0; k < kBk; k += 2) {
+            const uint64_t v = f2_fma(f2_pack(x[k], x[k + 1]), s2, nm2);
+            const float p0 = ex2_approx(f2_lo(v)), p1 = ex2_approx(f2_hi(v));
+            rs2 = f2_add(rs2, f2_pack(p0, p1));
+            x[k / 2] = __uint_as_float(pack2<FP16>(p0, p1));
           }
-          exponentials();
+          rs = f2_lo(rs2) + f2_hi(rs2);
+          set = __any_sync(0xffffffffu, rs > kPgMove);
+          if (!set) break;
         }
+        if (!ok) break;
         ell += rs;
-        tmem_st32(tS, pw);
+        tmem_st32(tS, x);
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -507,7 +496,7 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
       const int sl = 2 * p.share + (p.first ? 1 : 0);
       const size_t at = whole ? orow : (size_t)sl * a.part.rows + qi * trows + r;
       float* part = (whole ? a.part.dense[p.kind] : a.part.slots) + at * kD;
-#pragma unroll
+#pragma unroll 1
       for (int cc = 0; cc < 128; cc += 32) {
         float o[32];
         tmem_ld32(tO + cc, o);
