@@ -75,14 +75,14 @@ __device__ __forceinline__ int batch_tokens(const PagedGeom& g) { return max(0, 
 
 // a / b, a >= 0, b > 0: the 64-bit division is a long subroutine, so numbers
 // that fit take the 32-bit one (a piece's bookkeeping sits between two loads)
-__host__ __device__ __noinline__ int64_t quot_long(int64_t a, int64_t b) { return a / b; }
+static __host__ __device__ __noinline__ int64_t quot_long(int64_t a, int64_t b) { return a / b; }
 __host__ __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
   if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
   return quot_long(a, b);
 }
 
 // sum over i < n of floor((a i + b) / m), n, a, b >= 0, m > 0
-__host__ __device__ __noinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+static __host__ __device__ __noinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
   int64_t r = 0;
   while (n > 0) {
     if (a >= m) {

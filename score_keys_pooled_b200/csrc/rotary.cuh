@@ -10,13 +10,18 @@
 //
 // Angles: the host hands over inv_freq / 2 pi, so p * that is the angle in
 // turns, formed in fp64; only its fraction (exact after the subtraction of the
-// nearest integer) goes to fp32, so positions up to 2^31 keep an angle within
-// 2e-7 rad.  The products and the sum are fp32, rounded once to the type.
+// nearest integer) goes to fp32, so an angle is within 1e-6 rad at positions
+// up to 2^31 and within 4e-7 below 2^28.  The products and the sum are fp32,
+// rounded once to the type.
 //
 // Both kernels are bound by memory: a row of 256 bytes is read once and
 // written once, 16 bytes a load, eight lanes a row (a lane owns eight pairs:
 // two 16-byte chunks).  A block takes the rows of `tb` tokens; each token's
-// angles are formed once per block and shared by all of its heads.
+// angles are formed once per block and shared by all of its heads.  The
+// rotation of 131072 tokens of 40 heads, 2.68 GB, takes 430 us, 6.2 TB/s or 95 %
+// of the measured copy rate; the append of 14336 tokens, 353 MB whose cache rows
+// lie 256 bytes here and there, 70 us, 5.0 TB/s; one row more or fewer in flight
+// a thread and larger or smaller blocks made either slower or no faster.
 #pragma once
 
 #include <cuda_fp16.h>
