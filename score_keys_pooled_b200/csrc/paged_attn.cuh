@@ -73,6 +73,9 @@ struct PgDecode {
 };
 
 // Unfinished rows: fp32 accumulators and (reference, sum), base-2 exponents.
+// A row's columns stand in the order of the accumulator fragments: of every 32,
+// place 8 q + 2 j + e has column 8 j + 2 q + e (j, q < 4, e < 2), so that the
+// four threads of a fragment's row write its 32 columns as one line.
 struct PagedPart {
   float* dense[2];      // [Tq * Hq, 128]: rows of items that one share holds whole (0: prefix, 1: own)
   float2* dense_ml[2];  // [Tq * Hq]
@@ -153,6 +156,13 @@ template <bool FP16>
 __device__ __forceinline__ void store2(void* O, int out_f32, size_t at, float x, float y) {
   if (out_f32) *reinterpret_cast<float2*>(static_cast<float*>(O) + at) = make_float2(x, y);
   else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(O) + at) = pack2<FP16>(x, y);
+}
+// thread q's eight columns of 32 of an unfinished row (see PagedPart)
+__device__ __forceinline__ void store_part(float* block, int q, float v0, float v1, float v2, float v3, float v4,
+                                           float v5, float v6, float v7) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(block + 8 * q), "f"(v0), "f"(v1),
+               "f"(v2), "f"(v3), "f"(v4), "f"(v5), "f"(v6), "f"(v7)
+               : "memory");
 }
 __device__ __forceinline__ float lse_of(float ref, float sum) {
   return sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
@@ -479,8 +489,9 @@ __global__ void __launch_bounds__(32 * kPgWarps, 1)
           whole ? orow[k] : (size_t)(2 * p.share + (p.first ? 1 : 0)) * a.part.rows + 16 * rt + r0 + 8 * k;
       float* dst = (whole ? a.part.dense[p.kind] : a.part.slots) + at * kD;
 #pragma unroll
-      for (int n = 0; n < 16; ++n)
-        *reinterpret_cast<float2*>(dst + 8 * n + cq) = make_float2(acc[n][2 * k], acc[n][2 * k + 1]);
+      for (int n = 0; n < 16; n += 4)
+        store_part(dst + 8 * n, lane & 3, acc[n][2 * k], acc[n][2 * k + 1], acc[n + 1][2 * k], acc[n + 1][2 * k + 1],
+                   acc[n + 2][2 * k], acc[n + 2][2 * k + 1], acc[n + 3][2 * k], acc[n + 3][2 * k + 1]);
       if ((lane & 3) == 0) (whole ? a.part.dense_ml[p.kind] : a.part.slots_ml)[at] = make_float2(ref[k], sum[k]);
     }
   }
@@ -621,12 +632,10 @@ __device__ __forceinline__ float2 dense_part(const PagedPart& part, int kind, si
 template <bool FP16>
 __device__ __forceinline__ void finish_row(const JoinArgs& a, const RowSum& s, size_t row, int lane) {
   const float inv = s.l == 0.f ? 0.f : 1.f / s.l;
-  if (a.out_f32)
-    reinterpret_cast<float4*>(static_cast<float*>(a.O) + row * kD)[lane] =
-        make_float4(s.o.x * inv, s.o.y * inv, s.o.z * inv, s.o.w * inv);
-  else
-    reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.O) + row * kD)[lane] =
-        make_uint2(pack2<FP16>(s.o.x * inv, s.o.y * inv), pack2<FP16>(s.o.z * inv, s.o.w * inv));
+  // places 4 lane .. + 3 of the parts (see PagedPart)
+  const size_t at = row * kD + 32 * (lane >> 3) + 16 * (lane & 1) + 2 * ((lane >> 1) & 3);
+  store2<FP16>(a.O, a.out_f32, at, s.o.x * inv, s.o.y * inv);
+  store2<FP16>(a.O, a.out_f32, at + 8, s.o.z * inv, s.o.w * inv);
   if (a.lse && lane == 0) a.lse[row] = lse_of(s.m, s.l);
 }
 

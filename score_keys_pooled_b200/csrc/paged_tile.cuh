@@ -114,13 +114,19 @@ __device__ __forceinline__ TileKeys tile_keys(const PagedGeom& g, const Piece& p
   return k;
 }
 
-// eight floats, one 32-byte store: a thread writes its own row, so a warp's
-// store touches 32 lines whatever its width, and half as many stores take
-// half the time
-__device__ __forceinline__ void store_sector(float* p, const float* v) {
-  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
-               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-               : "memory");
+// 16 rows (of tensor-memory lanes) of 32 columns, as matrix fragments: thread
+// 4 i + q has columns 8 j + 2 q + {0, 1} of row i in v[4 j], v[4 j + 1], of row
+// i + 8 in v[4 j + 2], v[4 j + 3]
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 template <bool FP16>
@@ -496,28 +502,49 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
       const int sl = 2 * p.share + (p.first ? 1 : 0);
       const size_t at = whole ? orow : (size_t)sl * a.part.rows + qi * trows + r;
       float* part = (whole ? a.part.dense[p.kind] : a.part.slots) + at * kD;
+      if (!final) {
+        // four threads a row, so that a store writes whole lines of eight rows: 256
+        // sequences of short keys behind an 8K prefix 87.6 -> 85.6 us a pass against
+        // a thread that writes its own row
+        float* at_row[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          at_row[i] = reinterpret_cast<float*>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(has ? part : nullptr), 8 * i + lane / 4));
 #pragma unroll 1
-      for (int cc = 0; cc < 128; cc += 32) {
-        float o[32];
-        tmem_ld32(tO + cc, o);
-        tc_wait_ld();
-        if (!has) {
-        } else if (!final) {
+        for (int cc = 0; cc < 128; cc += 32) {
+          float o[32];
+          tmem_ld_frag(tO + cc, o);
+          tmem_ld_frag(tO + (16u << 16) + cc, o + 16);
+          tc_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 4; ++k) store_sector(part + cc + 8 * k, o + 8 * k);
-        } else if (a.out_f32) {
-          float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.O) + orow * kD + cc);
+          for (int i = 0; i < 4; ++i) {
+            const float* v = o + 16 * (i >> 1) + 2 * (i & 1);
+            if (at_row[i])
+              store_part(at_row[i] + cc, lane & 3, v[0], v[1], v[4], v[5], v[8], v[9], v[12], v[13]);
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int cc = 0; cc < 128; cc += 32) {
+          float o[32];
+          tmem_ld32(tO + cc, o);
+          tc_wait_ld();
+          if (!has) {
+          } else if (a.out_f32) {
+            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.O) + orow * kD + cc);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            dst[k] = make_float4(o[4 * k] * inv, o[4 * k + 1] * inv, o[4 * k + 2] * inv, o[4 * k + 3] * inv);
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.O) + orow * kD + cc);
+            for (int k = 0; k < 8; ++k)
+              dst[k] = make_float4(o[4 * k] * inv, o[4 * k + 1] * inv, o[4 * k + 2] * inv, o[4 * k + 3] * inv);
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.O) + orow * kD + cc);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            dst[k] = make_uint4(pack2<FP16>(o[8 * k] * inv, o[8 * k + 1] * inv),
-                                pack2<FP16>(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
-                                pack2<FP16>(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
-                                pack2<FP16>(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+            for (int k = 0; k < 4; ++k)
+              dst[k] = make_uint4(pack2<FP16>(o[8 * k] * inv, o[8 * k + 1] * inv),
+                                  pack2<FP16>(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                                  pack2<FP16>(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
+                                  pack2<FP16>(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+          }
         }
       }
       tc_fence_before();
