@@ -136,11 +136,25 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+__device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar,
+                                              uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1, {%2, %3}], [%4], %5;\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
       : "memory");
+}
+// L2 policies.  Keys that one worker (or one team, at about the same time) reads
+// go first when L2 is full: they leave the kernels' code and the parts there.
+// Fetched from memory, the code alone held every CTA up for 8 us (64 sequences
+// of up to 1023 keys behind 32K: 85.5 us a pass with no hint, 75.8 so).  Keys
+// that several items read stay as long as others (five prompt chunks of up to
+// 1023 tokens behind 8K: 440 us; 505 if theirs go first, too).
+__device__ __forceinline__ uint64_t keys_policy(bool once) {
+  uint64_t first, normal;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;\n" : "=l"(first));
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;\n" : "=l"(normal));
+  return once ? first : normal;
 }
 // Programmatic launch: the kernel behind this one may start on SMs that this
 // one leaves; and the wait until the kernel in front is done and its writes
@@ -262,6 +276,7 @@ __global__ void __launch_bounds__(32 * kPgWarps, 1)
   const int32_t* list = nullptr;
   SplitItem split = {0, 0, 0, 0};
   const int sub_log2 = g.page_log2 - 4;  // 16-key parts of a page
+  const uint64_t own_policy = keys_policy(true), prefix_policy = keys_policy(false);
   bool ok = true;
   auto issue = [&]() {
     if (ip.kind < 0) return;
@@ -305,7 +320,7 @@ __global__ void __launch_bounds__(32 * kPgWarps, 1)
       const int half = lane & 1, isv = lane >> 1;
       const int y = ((pg * g.Hkv + ip.kvh) << g.page_log2) + ((sub & ((1 << sub_log2) - 1)) << 4);
       tma_load_rows(ring + st * kPgStage + isv * (kPgSub * 256) + half * (kPgSub * 128), isv ? &tmV : &tmK, 64 * half,
-                    y, full(st));
+                    y, full(st), keys == 1 ? own_policy : prefix_policy);
     }
     ++sub;
     ++put;

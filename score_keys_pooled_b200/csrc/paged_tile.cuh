@@ -203,6 +203,8 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
     const int bi = lane >> 1, half = lane & 1;  // this lane's box of a tile
     bool ok = true;
     uint32_t it = 0, vt = 0;
+// own chunks are read by tile after tile, and the prefix by all of them
+    const uint64_t policy = keys_policy(!a.c.own_items && (sc.npt <= 1 || sc.team > 1));
     SplitItem split = {0, 0, 0, 0};
     for (int pi = 0; ok; ++pi) {
       Piece p;
@@ -244,7 +246,7 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
         if (bi < nb) {
           const int in_page = (((k.key0 >> box_log2) + bi) & ((1 << rest_log2) - 1)) << box_log2;
           tma_load_rows(ring + st * kTile2Bytes + half * (128 * 128) + (bi << box_log2) * 128, tm, 64 * half,
-                        ((page * g.Hkv + p.kvh) << g.page_log2) + in_page, full);
+                        ((page * g.Hkv + p.kvh) << g.page_log2) + in_page, full, policy);
         }
         if (ragged) {
           const bool landed = warp_ok(mbar_wait_bounded(full, vt & 1));
