@@ -98,6 +98,11 @@ PagedPlan paged_plan(const s2o_cache_config* c, int sms) {
   p.tile.kt_log2 = 7;
   p.decode.tpt = std::max(1, 16 * p.R / G);
   p.decode.kt_log2 = 6;
+  // what a piece costs beside its keys (see `fixed`): in the tile kernel 4 us,
+  // the row sums' way out of tensor memory (33 sequences of 40 rows, 700 keys,
+  // behind 5001: 36.9, 34.4, 32.8, 34.0 us with 0, 1, 2, 3 units)
+  p.tile.fixed = 2;
+  p.decode.fixed = 1;
   PagedCut& own = p.chunks ? p.tile : p.decode;
   own.own_items = 1;
   // microseconds
@@ -327,7 +332,7 @@ s2o_status s2o_attention_paged(const s2o_cache_config* cfg, const uint16_t* Q, c
   a.out_f32 = out_dtype == S2O_OUT_F32;
   a.direct = p.direct;
   a.beside = p.tiles;
-  a.own_ns = p.R == 1 ? 700.f : 1000.f;
+  a.own_ns = p.R == 1 ? 520.f : 1100.f;
   CUtensorMap tmQ, tmK, tmV;
   const uint64_t rows = (uint64_t)cfg->num_pages * cfg->Hkv * cfg->page_size;
   const uint32_t box = (uint32_t)std::min(cfg->page_size, 64);

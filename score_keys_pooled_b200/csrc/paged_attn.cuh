@@ -679,12 +679,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 8) k_paged_join(const __grid_
   if (!a.direct) {
     const PagedCut& c = a.prefix.c;
     const int npt = (ntok + c.tpt - 1) / c.tpt, rt = t / c.tpt;
-    const int64_t np = ((int64_t)g.prefix + (1 << c.kt_log2) - 1) >> c.kt_log2;
+    const int64_t np = prefix_units(g.prefix, c);
     const int workers = max(1, min((int)PW, a.prefix.n));
     team = team_size(c, npt, workers);
     const int n = shares_of(PU, workers / team);
     const int64_t u0 = (team > 1 ? (int64_t)kvh : (int64_t)kvh * npt + rt) * np;
-    c0 = share_owner(PU, n, u0);
+    c0 = share_owner(PU, n, u0 + c.fixed);  // of the first keys
     parts = share_owner(PU, n, u0 + np - 1) - c0 + 1;
     member = team > 1 ? rt : 0;
     prow = (t - rt * c.tpt) * g.G + hh;

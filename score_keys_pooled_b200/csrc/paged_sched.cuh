@@ -10,7 +10,9 @@
 //                  the sequence's own keys, causal; with `walk_prefix` the
 //                  prefix keys come first in the same item (long chunks fill
 //                  a tile by themselves, so nothing has to be joined later).
-// A unit is one tile of kt keys of an item.  The U units, in the order prefix
+// A unit is one tile of kt keys of an item, and `fixed` more at the item's
+// front stand for what an item costs whatever its length (2.2 us against 3.2 us
+// of a unit in the decode kernel).  The U units, in the order prefix
 // items (kvh, row tile), own items (sequence, kvh, row tile), are cut into n
 // even shares: share c takes units [c U / n, (c + 1) U / n), so the split
 // follows the actual lengths, which only the device knows, and every share
@@ -46,6 +48,7 @@ struct PagedCut {
   int prefix_items; // prefix items exist
   int own_items;    // own items exist
   int walk_prefix;  // own items start with the prefix's tiles
+  int fixed;        // units of an item that are no keys
 };
 
 struct SeqInfo {
@@ -108,13 +111,13 @@ struct OwnUnits {
   int nrt;       // row tiles
   int np;        // prefix tiles of each (walk_prefix)
   int len, off;  // own keys; own keys before the first new token
-  int tpt, kt_log2;
+  int tpt, kt_log2, fixed;
   // units of the first rt row tiles: tile i < nrt - 1 sees off + (i + 1) tpt keys, the last one all
   __host__ __device__ int64_t before(int rt) const {
     if (rt <= 0) return 0;
     const int64_t kt = (int64_t)1 << kt_log2;
-    if (nrt == 1) return np + ((len + kt - 1) >> kt_log2);
-    int64_t u = (int64_t)rt * np + floor_sum(rt < nrt ? rt : rt - 1, kt, tpt, (int64_t)off + tpt + kt - 1);
+    if (nrt == 1) return fixed + np + ((len + kt - 1) >> kt_log2);
+    int64_t u = (int64_t)rt * (fixed + np) + floor_sum(rt < nrt ? rt : rt - 1, kt, tpt, (int64_t)off + tpt + kt - 1);
     if (rt >= nrt) u += (len + kt - 1) >> kt_log2;
     return u;
   }
@@ -128,7 +131,13 @@ __host__ __device__ __forceinline__ OwnUnits own_units(int qlen, int len, int pr
   u.off = len - qlen;
   u.tpt = c.tpt;
   u.kt_log2 = c.kt_log2;
+  u.fixed = c.fixed;
   return u;
+}
+
+// units of a prefix item
+__host__ __device__ __forceinline__ int64_t prefix_units(int prefix, const PagedCut& c) {
+  return c.fixed + (((int64_t)prefix + (1 << c.kt_log2) - 1) >> c.kt_log2);
 }
 
 __host__ __device__ __forceinline__ int shares_of(int64_t U, int workers) { return U < workers ? (int)U : workers; }
@@ -238,14 +247,15 @@ __device__ __forceinline__ OwnRun own_run(const PagedGeom& g, const PagedCut& c,
 // by side: of `sms` SMs the decode kernel gets a share that makes both end
 // together.  A prefix unit (256 rows, 128 keys) keeps an SM 2250 ns busy (1300
 // with 128 rows); an own unit (64 keys, 32 KB) costs an SM of eight or four
-// streams 700 or 1000 ns (64 sequences of 512 keys behind 32K: 92, 84, 85, 99 us at 500,
-// 700, 900, 1200; one after the other on all SMs: 110).  Both kernels come to
-// the same answer.
+// streams 520 or 1100 ns (64 sequences of up to 1023 keys behind 32K: 71.8,
+// 69.4, 71.5, 74.9 us at 400, 480, 560, 700; 128 of 600 behind 8K: 59.4, 57.2,
+// 60.1 at 420, 520, 620; 64 of 5 tokens and 500 keys behind 16K, four streams:
+// 125, 117, 121 at 900, 1100, 1300).  Both kernels come to the same answer.
 constexpr float kTileNs = 2250.f, kHalfTileNs = 1300.f;
 __device__ __forceinline__ int decode_sms(const PagedGeom& g, const PagedCut& tile, int ntok, int64_t own_units,
                                           float own_ns, int sms) {
   const int npt = (ntok + tile.tpt - 1) / tile.tpt;
-  const int64_t np = ((int64_t)g.prefix + (1 << tile.kt_log2) - 1) >> tile.kt_log2;
+  const int64_t np = prefix_units(g.prefix, tile);
   const float w1 = (float)((int64_t)npt * g.Hkv * np) * (2 * ntok <= tile.tpt ? kHalfTileNs : kTileNs);
   const float w2 = (float)own_units * own_ns;
   const int n = __float2int_rn((float)sms * w2 / (w1 + w2));
@@ -263,7 +273,7 @@ __device__ __forceinline__ Sched sched_begin(const PagedGeom& g, const PagedCut&
   const bool works = blockIdx.x < ctas;
   s.ntok_all = batch_tokens(g);
   s.npt = c.prefix_items ? (s.ntok_all + c.tpt - 1) / c.tpt : 0;
-  const int64_t np = ((int64_t)g.prefix + (1 << c.kt_log2) - 1) >> c.kt_log2;
+  const int64_t np = prefix_units(g.prefix, c);
   s.team = team_size(c, s.npt, workers);
   if (s.team > 1) {
     s.U = g.Hkv * np;
@@ -366,11 +376,15 @@ __device__ __forceinline__ Piece sched_next(const PagedGeom& g, const PagedCut& 
   p.share = s.team > 1 ? s.me * s.team + s.rt : s.me;
   p.seq = s.seq;
   p.kvh = s.kvh;
-  p.tile0 = (int)(s.u - s.item0);
+  p.tile0 = (int)max((int64_t)0, s.u - s.item0 - c.fixed);
   const int64_t stop = min(s.end, s.item0 + s.items);
-  p.tile1 = (int)(stop - s.item0);
+  if (stop - s.item0 <= c.fixed) {  // the share ends before the item's first keys
+    p.kind = s.kind = -1;
+    return p;
+  }
+  p.tile1 = (int)(stop - s.item0 - c.fixed);
   p.first = p.tile0 == 0;
-  p.last = p.tile1 == s.items;
+  p.last = stop == s.item0 + s.items;
   if (s.kind == 0) {
     p.tok0 = s.rt * c.tpt;
     p.ntok = min(c.tpt, s.ntok_all - p.tok0);
