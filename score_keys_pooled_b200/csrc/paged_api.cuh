@@ -75,12 +75,18 @@ int sm_count() {
 // which reads the cache at 16 or 32 rows a key; more fill a tcgen05 tile well
 // enough (33 rows of 128 still keep up with the memory: 64 KB of keys in 1.3
 // us).  The prefix is then taken the cheapest of these ways, by what its units
-// cost (decode_sms has the figures; a join costs 5 us and 1.5 us a thousand
-// rows, a second kernel beside the first 10 us):
+// cost an SM (128 keys in the tile kernel 2.25 us, 1.3 with 128 rows; 64 in the
+// decode kernel 1.2 or, with four streams, 1.7, the join of its many parts
+// among it), a join 5 us and 1.5 us a thousand rows, a second kernel beside the
+// first 8.5 us:
 //   walk    each own item begins with the prefix: nothing to join, but every
 //           sequence reads it (from L2)
 //   items   prefix items in the same kernel: read once per row tile
 //   tiles   (decode) prefix items in the tile kernel beside it
+// Measured with each forced (walk, items, tiles; 32 heads on 8): 16 sequences of
+// 500 keys behind 1000 27.1, 24.7, 27.3 us, behind 4000 44, 29.7, 30.2, behind
+// 20000 134, 56, 40; 8 of 2000 behind 30000 109, 64, 46; one of 100 behind 130000
+// (4 KV heads) 75, 75, 64.
 struct PagedPlan {
   bool chunks;   // the tile kernel takes the own keys, otherwise the decode kernel
   bool tiles;    // decode: the tile kernel takes the prefix beside it
@@ -108,12 +114,13 @@ PagedPlan paged_plan(const s2o_cache_config* c, int sms) {
   // microseconds
   const double prefix = c->prefix_len, tokens = c->Tq, seqs = std::min(c->nseq, std::max(c->Tq, 1));
   const double units = c->Hkv * std::ceil(prefix / (1 << own.kt_log2)) / sms;
-  const double unit = p.chunks ? (2 * c->max_q <= p.tile.tpt ? 1.3 : 2.25) : (p.R == 1 ? 0.6 : 0.9);
+  const double unit = p.chunks ? (2 * c->max_q <= p.tile.tpt ? 1.3 : 2.25) : (p.R == 1 ? 1.2 : 1.7);
+  const double tile = 2 * tokens <= p.tile.tpt ? 1.3 : 2.25;
   const double join = 5 + 1.5e-3 * tokens * c->Hq;
   const double walk = units * unit * (seqs + std::floor((tokens - seqs) / own.tpt));
   const double items = units * (p.chunks ? 2.25 : unit) * std::ceil(tokens / own.tpt) + join;
   const double tiles = p.chunks ? INFINITY
-                                : c->Hkv * std::ceil(prefix / 128) / sms * std::ceil(tokens / p.tile.tpt) * 2.25 + join + 10;
+                                : c->Hkv * std::ceil(prefix / 128) / sms * std::ceil(tokens / p.tile.tpt) * tile + join + 8.5;
   p.direct = c->prefix_len == 0 || (walk <= items && walk <= tiles);
   p.tiles = !p.direct && tiles < items;
   own.walk_prefix = p.direct && c->prefix_len > 0;
