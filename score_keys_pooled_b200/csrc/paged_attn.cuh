@@ -16,10 +16,10 @@
 //     stages per SM), and its first warp issues the TMA boxes itself, each
 //     into the stage that the stream has just read.  A stage costs a stream 0.7
 //     to 0.9 us of latency (two chains of products with the softmax between)
-//     and a piece some us (sequence numbers, first loads, results), while the
+//     and a piece 2.2 us (sequence numbers, first loads, results), while the
 //     other streams' reads go on: 16 sequences of up to 32K keys, 1.07 GB, take
 //     180 us, 6.0 TB/s, 91 % of the measured copy rate; even shares on SMs that
-//     are not equally near the memory (warps end between 128 and 173 us) are
+//     are not equally near the memory (warps end between 119 and 174 us) are
 //     what is left.  One ring for the whole CTA, its 64-key stages cut into
 //     slices over four or eight warps and joined in shared memory at the end of
 //     each piece, spent 8 to 13 us at every piece boundary: 58 and 79 us on 64
