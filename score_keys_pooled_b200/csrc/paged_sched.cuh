@@ -62,11 +62,8 @@ __device__ __forceinline__ SeqInfo seq_info(const PagedGeom& g, int s) {
   i.q0 = g.q_start[s];
   const int q1 = g.q_start[s + 1];
   i.len = g.kv_len[s];
-  const int64_t n = (int64_t)q1 - i.q0;
-  i.qlen = (int)n;
-  if (n == 0 && (s > 0 || i.q0 == 0)) return i;
-  if (i.q0 < 0 || (s == 0 && i.q0 != 0) || n < 0 || q1 > g.Tq || n > g.max_q || i.len < n ||
-      i.len > ((int64_t)g.max_pages << g.page_log2)) {
+  i.qlen = (int)((int64_t)q1 - i.q0);
+  if (!seq_fits(s, i.q0, q1, i.len, g.Tq, g.max_q, (int64_t)g.max_pages << g.page_log2)) {
     set_error(kErrBadCache);
     i.qlen = 0;
   }

@@ -171,6 +171,15 @@ struct AppendArgs {
   int Hq, Hkv, page_log2, num_pages, nseq, max_pages, Tq, max_q, prefix, tb;
 };
 
+// A sequence's numbers, as a call may find them on the device: tokens [q0, q1)
+// behind one another from 0 to at most Tq, at most max_q of them, `len` own keys
+// that hold them and fit the table.  A sequence without tokens needs no length.
+__device__ __forceinline__ bool seq_fits(int s, int q0, int q1, int len, int Tq, int max_q, int64_t room) {
+  const int64_t n = (int64_t)q1 - q0;
+  if (q0 < 0 || (s == 0 && q0 != 0) || n < 0 || q1 > Tq) return false;
+  return n == 0 || (n <= max_q && len >= n && len <= room);
+}
+
 // the sequence of token t: the last s with q_start[s] <= t (q_start[0] <= t)
 __device__ __forceinline__ int seq_of_token(const int32_t* q_start, int nseq, int t) {
   int lo = 0, hi = nseq;  // q_start[lo] <= t; the answer is in [lo, hi)
@@ -187,19 +196,22 @@ __global__ void __launch_bounds__(kRotThreads) k_cache_append(const __grid_const
   __shared__ int32_t pos[kRotMaxTokens][3];
   __shared__ int64_t slot[kRotMaxTokens];  // row of head 0 in the caches; -1: no write
   const int t0 = blockIdx.x * a.tb;
+  const int64_t room = (int64_t)a.max_pages << a.page_log2;
+  // The blocks check every sequence between them, those that none of the tokens
+  // below leads to as well.  The first warp has the tokens; the others' reads
+  // are on their way beside its own.
+  if (threadIdx.x >= 32)
+    for (int64_t s = (int64_t)blockIdx.x * (kRotThreads - 32) + threadIdx.x - 32; s < a.nseq;
+         s += (int64_t)gridDim.x * (kRotThreads - 32))
+      if (!seq_fits((int)s, a.q_start[s], a.q_start[s + 1], a.kv_len[s], a.Tq, a.max_q, room)) set_error(kErrBadCache);
   const int ntok = min(min(a.tb, a.Tq - t0), a.q_start[a.nseq] - t0);  // tokens behind the last sequence: none
-  if (ntok <= 0) {
-    if (threadIdx.x == 0 && a.q_start[a.nseq] < 0) set_error(kErrBadCache);
-    return;
-  }
+  if (ntok <= 0) return;
   if (threadIdx.x < ntok) {
     const int t = t0 + threadIdx.x;
     const int s = seq_of_token(a.q_start, a.nseq, t);
     const int q0 = a.q_start[s], q1 = a.q_start[s + 1], len = a.kv_len[s];
     const int64_t at = (int64_t)len - q1 + t;  // place among the sequence's own keys
-    // a start that is not ascending, more tokens than stated, a length over the table
-    bool ok = q0 >= 0 && q0 <= t && t < q1 && q1 <= a.Tq && q1 - q0 <= a.max_q && len >= q1 - q0 &&
-              len <= ((int64_t)a.max_pages << a.page_log2);
+    bool ok = q0 <= t && t < q1 && seq_fits(s, q0, q1, len, a.Tq, a.max_q, room);
     int64_t row = -1;
     if (ok) {
       const int page = a.table[(int64_t)s * a.max_pages + (at >> a.page_log2)];

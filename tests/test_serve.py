@@ -260,6 +260,32 @@ def test_append_flags_bad_pages_and_lengths_and_writes_nothing_there():
         assert torch.equal(kc.cpu()[own0].view(torch.int16), b.k[own0].view(torch.int16)), what
 
 
+def test_append_flags_ranges_that_none_of_its_tokens_leads_to():
+    """A sequence that lies behind the rows, descending starts, starts that do not
+    begin at 0, one bad entry among hundreds of sequences without tokens: flagged
+    as the attention flags them, and cache rows of nobody stay."""
+    for qs, kl in (([0, 4, 1000], [9, 9]), ([0, 4, 2], [9, 9]), ([0, 0, -1], [9, 9]), ([2, 2, 2], [9, 9]),
+                   ([0, 2, 4] + [4] * 298 + [6], [9] * 301), ([0] * 200 + [-3] + [0] * 100 + [4], [9] * 301)):
+        nseq = len(kl)
+        b = Batch([4] + [0] * (nseq - 1), [9] * nseq, max_q=8)
+        qs, kl, table = (torch.tensor(x, dtype=torch.int32).cuda() for x in (qs, kl, b.table.tolist()))
+        x = torch.randn(4, 2, 128, device="cuda").bfloat16()
+        kc, vc = b.k.cuda(), b.v.cuda()
+        s2o.cache_append(b.cfg, None, x, x, kc, vc, table, qs, kl)
+        assert s2o.last_device_error() == BAD_CACHE, qs.tolist()[:4]
+        free = [i for i in range(b.cfg.num_pages) if i not in b.table.flatten().tolist()]
+        assert torch.equal(kc.cpu()[free].view(torch.int16), b.k[free].view(torch.int16))
+        s2o.attention_paged(b.cfg, torch.zeros(4, 8, 128, device="cuda").bfloat16(), torch.nan_to_num(kc),
+                            torch.nan_to_num(vc), table, qs, kl)
+        assert s2o.last_device_error() == BAD_CACHE, qs.tolist()[:4]
+    b = Batch([0] * 150 + [4] + [0] * 150, [9] * 301)  # sequences without tokens need no length
+    kl = torch.where(torch.arange(301) == 150, 9, -7).int().cuda()
+    kc, vc = b.k.cuda(), b.v.cuda()
+    s2o.cache_append(b.cfg, None, x, x, kc, vc, b.table.cuda(), b.q_start.cuda(), kl)
+    assert s2o.last_device_error() == 0
+    assert torch.equal(kc[b.table[150, 0].long(), :, 5:9], x.transpose(0, 1))
+
+
 # --- attention ----------------------------------------------------------------------------------------
 
 CASES = {
