@@ -173,11 +173,12 @@ struct AppendArgs {
 
 // A sequence's numbers, as a call may find them on the device: tokens [q0, q1)
 // behind one another from 0 to at most Tq, at most max_q of them, `len` own keys
-// that hold them and fit the table.  A sequence without tokens needs no length.
+// that hold them and fit the table.  One without tokens needs no length, and its
+// place is its neighbours' to answer for.
 __device__ __forceinline__ bool seq_fits(int s, int q0, int q1, int len, int Tq, int max_q, int64_t room) {
   const int64_t n = (int64_t)q1 - q0;
-  if (q0 < 0 || (s == 0 && q0 != 0) || n < 0 || q1 > Tq) return false;
-  return n == 0 || (n <= max_q && len >= n && len <= room);
+  if (n == 0 && (s > 0 || q0 == 0)) return true;
+  return !(q0 < 0 || (s == 0 && q0 != 0) || n < 0 || q1 > Tq || n > max_q || len < n || len > room);
 }
 
 // the sequence of token t: the last s with q_start[s] <= t (q_start[0] <= t)
