@@ -74,19 +74,30 @@ int sm_count() {
 // Rows of a sequence's new tokens (max_q G) up to 32 go to the decode kernel,
 // which reads the cache at 16 or 32 rows a key; more fill a tcgen05 tile well
 // enough (33 rows of 128 still keep up with the memory: 64 KB of keys in 1.3
-// us).  The prefix is then taken the cheapest of these ways, by what its units
-// cost an SM (128 keys in the tile kernel 2.25 us, 1.3 with 128 rows; 64 in the
-// decode kernel 1.2 or, with four streams, 1.7, the join of its many parts
-// among it), a join 5 us and 1.5 us a thousand rows, a second kernel beside the
-// first 8.5 us:
-//   walk    each own item begins with the prefix: nothing to join, but every
-//           sequence reads it (from L2)
+// us).  The prefix is then taken the cheapest of these ways:
+//   walk    each own item begins with the prefix: one list of parts, but every
+//           item reads it (from L2 where it fits)
 //   items   prefix items in the same kernel: read once per row tile
 //   tiles   (decode) prefix items in the tile kernel beside it
-// Measured with each forced (walk, items, tiles; 32 heads on 8): 16 sequences of
-// 500 keys behind 1000 27.1, 24.7, 27.3 us, behind 4000 44, 29.7, 30.2, behind
-// 20000 134, 56, 40; 8 of 2000 behind 30000 109, 64, 46; one of 100 behind 130000
-// (4 KV heads) 75, 75, 64.
+// By what each costs beside the own keys, in microseconds:
+//   units   an SM's 128 keys in the tile kernel kTileNs, kHalfTileNs with 128
+//           rows (1.75 us where every item reads them for itself: 64 KB a unit
+//           on all SMs are 5.5 TB/s); 64 in the decode kernel 1.2, with four
+//           streams 1.7 (the join of a token's many parts among it)
+//   walk    the row tiles of ragged sequences are at most one each and one more
+//           for every tpt tokens, and at most the tiles of max_q each; in the
+//           tile kernel 0.2 for each part that few long items are cut into
+//   items   the second list of parts: 2 and 1.5 a thousand rows, in the tile
+//           kernel 2 and 0.5
+//   tiles   as items, and 8.5 for a second kernel beside the first
+// 561 shapes with each way forced (1 to 256 sequences of 1 to 1023 new tokens,
+// prefixes of 10 to 131072, groups of 1 to 8): the way taken is within 3 % of the
+// best on 505, 0.9 % behind it on average, 20 % at most (one chunk of 44 tokens
+// with 22000 own keys behind 89: 41.0 us where items take 34.0).  Walk, items,
+// tiles at 32 heads on 8: 16 sequences of one token behind 1000 26.0, 23.4, 24.6 us,
+// behind 4000 43, 27.5, 27.8, behind 20000 134, 54, 39; 16 of 4 tokens behind 1000
+// 28.0, 27.1, 25.1; 32 chunks of 64 behind 8000 271, 303, behind 32768 1091, 1130;
+// one of 512 and 63 single tokens behind 8192 539, 136.
 struct PagedPlan {
   bool chunks;   // the tile kernel takes the own keys, otherwise the decode kernel
   bool tiles;    // decode: the tile kernel takes the prefix beside it
@@ -97,7 +108,8 @@ struct PagedPlan {
 PagedPlan paged_plan(const s2o_cache_config* c, int sms) {
   PagedPlan p{};
   const int G = c->Hq / c->Hkv;
-  const int64_t seq_rows = (int64_t)std::min(c->max_q, std::max(c->Tq, 1)) * G;
+  const int max_q = std::min(c->max_q, std::max(c->Tq, 1));
+  const int64_t seq_rows = (int64_t)max_q * G;
   p.chunks = seq_rows > 32;
   p.R = seq_rows <= 16 ? 1 : 2;
   p.tile.tpt = 2 * (kLq / G);
@@ -114,13 +126,20 @@ PagedPlan paged_plan(const s2o_cache_config* c, int sms) {
   // microseconds
   const double prefix = c->prefix_len, tokens = c->Tq, seqs = std::min(c->nseq, std::max(c->Tq, 1));
   const double units = c->Hkv * std::ceil(prefix / (1 << own.kt_log2)) / sms;
-  const double unit = p.chunks ? (2 * c->max_q <= p.tile.tpt ? 1.3 : 2.25) : (p.R == 1 ? 1.2 : 1.7);
-  const double tile = 2 * tokens <= p.tile.tpt ? 1.3 : 2.25;
-  const double join = 5 + 1.5e-3 * tokens * c->Hq;
-  const double walk = units * unit * (seqs + std::floor((tokens - seqs) / own.tpt));
-  const double items = units * (p.chunks ? 2.25 : unit) * std::ceil(tokens / own.tpt) + join;
-  const double tiles = p.chunks ? INFINITY
-                                : c->Hkv * std::ceil(prefix / 128) / sms * std::ceil(tokens / p.tile.tpt) * tile + join + 8.5;
+  const double tile = (2 * tokens <= p.tile.tpt ? kHalfTileNs : kTileNs) * 1e-3, krows = 1e-3 * tokens * c->Hq;
+  const double own_tiles = std::min(seqs + std::floor((tokens - seqs) / own.tpt), seqs * std::ceil((double)max_q / own.tpt));
+  const double tok_tiles = std::ceil(tokens / own.tpt);
+  double walk, items, tiles = INFINITY;
+  if (p.chunks) {
+    const double parts = std::min(sms / (own_tiles * c->Hkv), std::ceil(prefix / 128) + own.fixed);
+    walk = units * own_tiles * (2 * max_q <= own.tpt ? 1.75 : kTileNs * 1e-3) + 0.2 * std::max(0., parts - 1);
+    items = units * tok_tiles * tile + 2 + 0.5 * krows;
+  } else {
+    const double unit = p.R == 1 ? 1.2 : 1.7, join = 2 + 1.5 * krows;
+    walk = units * own_tiles * unit;
+    items = units * tok_tiles * unit + join;
+    tiles = c->Hkv * std::ceil(prefix / 128) / sms * std::ceil(tokens / p.tile.tpt) * tile + join + 8.5;
+  }
   p.direct = c->prefix_len == 0 || (walk <= items && walk <= tiles);
   p.tiles = !p.direct && tiles < items;
   own.walk_prefix = p.direct && c->prefix_len > 0;

@@ -247,7 +247,8 @@ __device__ __forceinline__ OwnRun own_run(const PagedGeom& g, const PagedCut& c,
 // streams 520 or 1100 ns (64 sequences of up to 1023 keys behind 32K: 71.8,
 // 69.4, 71.5, 74.9 us at 400, 480, 560, 700; 128 of 600 behind 8K: 59.4, 57.2,
 // 60.1 at 420, 520, 620; 64 of 5 tokens and 500 keys behind 16K, four streams:
-// 125, 117, 121 at 900, 1100, 1300).  Both kernels come to the same answer.
+// 125, 117, 121 at 900, 1100, 1300).  Both kernels come to the same answer; the
+// host's choice between the prefix's ways goes by the same prices of a tile.
 constexpr float kTileNs = 2250.f, kHalfTileNs = 1300.f;
 __device__ __forceinline__ int decode_sms(const PagedGeom& g, const PagedCut& tile, int ntok, int64_t own_units,
                                           float own_ns, int sms) {

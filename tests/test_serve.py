@@ -23,6 +23,7 @@ import torch
 import score_keys_pooled_b200 as s2o
 from score_keys_pooled_b200 import synth
 from oracle import serve_oracle as SO
+from tests import serve_ways as ways
 
 pytestmark = pytest.mark.gpu
 
@@ -422,6 +423,20 @@ def test_every_way_of_the_attention(way, t):
         O2, lse2 = s2o.attention_paged(b.cfg, q, k, v, table, qs, kl, prefix_pages=pre, workspace=ws)
         attend(c)
         assert torch.equal(O2[:b.own], O[:b.own]) and torch.equal(lse2[:b.own], lse[:b.own])
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp16"])
+def test_equal_chunks_walk_the_prefix(t):
+    """Chunks of equal length go tile by tile through prefix and own keys: two
+    launches, no second list of parts."""
+    b = Batch([64] * 16, [64 + 31 * i for i in range(16)], 8190, 64, 8, 2, TYPES[t], seed=21, extra_rows=1)
+    assert ways.way(b.cfg) == "chunks walk"
+    q, k, v, table, qs, kl, pre = b.dev()
+    ws = s2o.alloc_attention_paged(b.cfg).fill_(255)
+    O, lse = s2o.attention_paged(b.cfg, q, k, v, table, qs, kl, prefix_pages=pre, workspace=ws)
+    assert s2o.last_launch_count() == 2 and s2o.last_device_error() == 0
+    b.want = dense_reference(b, q, k, v, table, kl, pre)
+    b.check(O, lse)
 
 
 def test_a_batch_without_tokens():

@@ -9,6 +9,7 @@ import torch
 import score_keys_pooled_b200 as s2o
 from score_keys_pooled_b200 import build
 from oracle import serve_oracle as SO
+from tests import serve_ways as ways
 
 GOOD = ctypes.c_void_p(1 << 20)
 ODD = ctypes.c_void_p((1 << 20) + 8)
@@ -96,6 +97,39 @@ def test_cache_config_validation(L, change, code):
     assert L.s2o_attention_paged(c, GOOD, GOOD, GOOD, GOOD, GOOD, GOOD, GOOD, GOOD, 0, None, GOOD, 1 << 40, None) == code
     assert L.s2o_cache_append(c, None, None, view(), view(), None, GOOD, GOOD, GOOD, GOOD, GOOD, None, None) == code
     assert s2o.last_launch_count() == 0
+
+
+@pytest.mark.parametrize("nseq,max_q,Tq,prefix,heads,want,mb", [
+    # equal chunks: the row tiles of the walk are those of the items, which join a second list
+    (32, 64, 32 * 64, 32768, (32, 8), "chunks walk", 39.1), (16, 256, 16 * 256, 32768, (32, 8), "chunks walk", 39.1),
+    (8, 128, 8 * 128, 16384, (32, 8), "chunks walk", 39.1), (16, 64, 16 * 64, 8192, (32, 8), "chunks walk", 39.1),
+    # one chunk among single tokens: the host knows 64 + floor(511 / 64) tiles at most
+    (64, 512, 512 + 63, 8192, (32, 8), "chunks items", 58.4),
+    (20, 40, 800, 1500, (8, 8), "chunks items", 46.1), (33, 5, 165, 5001, (16, 2), "chunks items", 42.0),
+    (16, 4, 64, 1000, (32, 8), "decode1 tiles", 61.0), (32, 5, 160, 8192, (32, 8), "decode2 tiles", 64.0),
+    (16, 1, 16, 20000, (32, 8), "decode1 tiles", None), (1, 1, 1, 1024, (32, 8), "decode1 walk", None),
+    (1, 1, 1, 0, (32, 8), "decode1 walk", None),
+])
+def test_the_way_of_the_prefix(L, nseq, max_q, Tq, prefix, heads, want, mb):
+    c = s2o.make_cache(*heads, page_size=64, num_pages=4096, nseq=nseq, max_pages=40, Tq=Tq, max_q=max_q,
+                       prefix_len=prefix)
+    assert ways.way(c) == want
+    if mb:
+        assert abs(ways.sizes(c)[want] / 1e6 - mb) < 1.0
+
+
+def test_the_gpu_tests_reach_the_ways_they_name(L):
+    from tests.test_serve import WAYS
+    want = {"decode_walks_prefix": "decode1 walk", "decode_two_row_tiles": "decode2 walk",
+            "decode_prefix_items": "decode1 items", "tiles_in_teams": "decode1 tiles",
+            "tiles_in_teams_ragged": "decode1 tiles", "tiles_without_teams": "decode2 tiles",
+            "tiles_of_128_rows": "decode1 tiles", "chunks_walk_prefix": "chunks walk",
+            "chunks_prefix_items": "chunks items", "chunks_alone_long": "chunks walk",
+            "chunk_groups_of_48": "chunks walk"}
+    for name, (new, length, P, page, Hq, Hkv, _) in WAYS.items():
+        c = s2o.make_cache(Hq, Hkv, page, 1 << 14, len(new), max(1, max(length) // page + 1), sum(new) + 1,
+                           max_q=max(new), prefix_len=P)
+        assert ways.way(c) == want[name], name
 
 
 def test_attention_paged_refusals(L):
