@@ -439,6 +439,37 @@ def test_equal_chunks_walk_the_prefix(t):
     b.check(O, lse)
 
 
+# the decode kernel with two row tiles and the prefix in its own streams: both key lists in one piece, their
+# border anywhere in a stage ring; (new, own keys, prefix, page, Hq, Hkv, way)
+TWO_ROW_TILES = {
+    "walk_drafts_of_8": ([5, 8, 6], [40, 8, 177], 77, 16, 32, 8, "decode2 walk"),
+    "walk_ragged": ([8, 1, 3, 0] * 8, [61, 500, 3, 90] * 8, 201, 64, 8, 2, "decode2 walk"),
+    "walk_one_key": ([5] * 6, [5, 6, 64, 65, 130, 400], 1, 16, 8, 2, "decode2 walk"),
+    "walk_group_of_20": ([1] * 9, [1 + 40 * i for i in range(9)], 499, 32, 40, 2, "decode2 walk"),
+    "walk_group_of_12": ([1, 2] * 6, [33, 64] * 6, 90, 128, 24, 2, "decode2 walk"),
+    "items": ([8] + [1] * 20, [9] + [1 + 17 * i for i in range(20)], 1001, 32, 8, 2, "decode2 items"),
+    "items_32_heads": ([7] + [1] * 20, [300] + [1 + 9 * i for i in range(20)], 1009, 64, 32, 8, "decode2 items"),
+}
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp16"])
+@pytest.mark.parametrize("name", list(TWO_ROW_TILES))
+def test_two_row_tiles_with_the_prefix_in_the_same_kernel(name, t):
+    new, length, P, page, Hq, Hkv, way = TWO_ROW_TILES[name]
+    b = Batch(new, length, P, page, Hq, Hkv, TYPES[t], seed=31, extra_rows=2)
+    assert ways.way(b.cfg) == way
+    O = torch.full((b.Tq, Hq, 128), 5.0, device="cuda", dtype=TYPES[t])
+    lse = torch.full((b.Tq, Hq), 5.0, device="cuda")
+    ws = s2o.alloc_attention_paged(b.cfg).fill_(255)
+    attend(b, O=O, lse=lse, workspace=ws)
+    assert s2o.last_launch_count() == 2
+    b.check(O, lse, name)
+    assert bool((O[b.own:] == 5.0).all()) and bool((lse[b.own:] == 5.0).all())
+    for _ in range(5):
+        O2, lse2 = attend(b, workspace=ws)
+        assert torch.equal(O2[:b.own], O[:b.own]) and torch.equal(lse2[:b.own], lse[:b.own])
+
+
 def test_a_batch_without_tokens():
     """No token at all, or rows that belong to nobody: nothing is written."""
     b = Batch([0, 0], [30, 0], 40)
