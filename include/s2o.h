@@ -402,7 +402,11 @@ typedef struct s2o_view {
  *   q, k         [B, N, Hq, 128] and [B, N, Hkv, 128] views; Hq or Hkv may be 0
  *   positions    device int32 [naxes, B, N]
  *   q_out, k_out views of the same extents; a view may be its own input
- *                (in place), other overlaps are not allowed
+ *                (in place).  Rows of an output must not share memory with one
+ *                another, the other output's or, elsewhere than in place, an
+ *                input's: S2O_ERR_INVALID_ARG, where the views have the same
+ *                strides or one of the two fills its memory (views of one buffer,
+ *                whole tensors); other interleavings are the caller's to avoid
  *   inverse      nonzero: turn by -phi (the transposed rotation, which also
  *                takes a gradient of the outputs to one of the inputs)
  */
@@ -412,7 +416,8 @@ s2o_status s2o_rotary(const s2o_rotary_config* rotary, int32_t dtype, int32_t B,
 
 /*
  * The paged cache of a batch.
- *   k_cache, v_cache  device [num_pages, Hkv, page_size, 128], 16-byte aligned
+ *   k_cache, v_cache  device [num_pages, Hkv, page_size, 128], 16-byte aligned,
+ *                     apart from one another
  *   page_table        device int32 [nseq, max_pages]: key i of sequence s is
  *                     row i % page_size of page page_table[s, i / page_size];
  *                     entries behind a sequence's last page are not read
@@ -448,7 +453,7 @@ typedef struct s2o_cache_config {
  * their pages, and turn their queries beside it.
  *   rotary     NULL: nothing is turned
  *   q, q_out   [Tq, Hq, 128] views (stride_b unused), both NULL: no queries;
- *              q_out may be q
+ *              q_out may be q; its other overlaps are those of s2o_rotary
  *   k, v       [Tq, Hkv, 128] views
  *   positions  device int32 [naxes, Tq], or NULL: token i of a sequence's own
  *              keys stands at prefix_len + i on every axis
@@ -465,7 +470,7 @@ s2o_status s2o_cache_append(const s2o_cache_config* cfg, const s2o_rotary_config
  * keys 0 .. i.  The prefix is read once for the whole batch, each own key once.
  *   Q    device [Tq, Hq, 128], contiguous
  *   O    out, device [Tq, Hq, 128], in the cache's type (S2O_OUT_SAME) or
- *        fp32; not Q's memory
+ *        fp32; apart from Q's memory
  *   lse  out, device fp32 [Tq, Hq]: log sum_j exp(s_ij); or NULL
  *   workspace  device scratch of s2o_attention_paged_workspace_size() bytes
  *        (on the device the call runs on), 256-byte aligned; contents need no

@@ -34,9 +34,15 @@ bool take_view(const s2o_view* v, RowView* out) {
   return true;
 }
 
-// an output whose rows fall on one another
-bool overlaps(const RowView& v, int64_t B, int64_t N, int64_t H) {
-  return (B > 1 && v.sb == 0) || (N > 1 && v.st == 0) || (H > 1 && v.sh == 0);
+// an output where the input it is made from has other rows: in place means in
+// every row's own place
+bool rows_clash(const RowView& out, const RowView& in, int64_t B, int64_t N, int64_t H) {
+  return !rows_same(out, in, B, N, H) && rows_meet(out, H, in, H, B, N);
+}
+// [a, a + an) and [b, b + bn) bytes share one
+bool ranges_meet(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + bn && y < x + an;
 }
 
 s2o_status check_cache(const s2o_cache_config* c) {
@@ -270,7 +276,12 @@ s2o_status s2o_rotary(const s2o_rotary_config* rotary, int32_t dtype, int32_t B,
   std::memset(&a.q, 0, 4 * sizeof(RowView));
   if (Hq && (!take_view(q, &a.q) || !take_view(q_out, &a.qo))) return S2O_ERR_INVALID_ARG;
   if (Hkv && (!take_view(k, &a.k) || !take_view(k_out, &a.ko))) return S2O_ERR_INVALID_ARG;
-  if ((Hq && overlaps(a.qo, B, N, Hq)) || (Hkv && overlaps(a.ko, B, N, Hkv))) return S2O_ERR_INVALID_ARG;
+  // rows are turned in any order: none may be written twice, or before another is made from it
+  if ((Hq && (rows_meet(a.qo, B, N, Hq) || rows_clash(a.qo, a.q, B, N, Hq))) ||
+      (Hkv && (rows_meet(a.ko, B, N, Hkv) || rows_clash(a.ko, a.k, B, N, Hkv))) ||
+      (Hq && Hkv && (rows_meet(a.qo, Hq, a.ko, Hkv, B, N) || rows_meet(a.qo, Hq, a.k, Hkv, B, N) ||
+                     rows_meet(a.q, Hq, a.ko, Hkv, B, N))))
+    return S2O_ERR_INVALID_ARG;
   a.pos = positions;
   a.B = B; a.N = N; a.Hq = Hq; a.Hkv = Hkv;
   const int64_t total = (int64_t)B * N;
@@ -301,8 +312,12 @@ s2o_status s2o_cache_append(const s2o_cache_config* cfg, const s2o_rotary_config
   if (!aligned16(k_cache) || !aligned16(v_cache)) return S2O_ERR_INVALID_ARG;
   std::memset(&a.q, 0, 4 * sizeof(RowView));
   if (!take_view(k, &a.k) || !take_view(v, &a.v)) return S2O_ERR_INVALID_ARG;
-  if (q && (!take_view(q, &a.q) || !take_view(q_out, &a.qo) || overlaps(a.qo, 1, cfg->Tq, cfg->Hq)))
+  const int T = cfg->Tq, Hq = cfg->Hq, Hkv = cfg->Hkv;
+  if (q && (!take_view(q, &a.q) || !take_view(q_out, &a.qo) || rows_meet(a.qo, 1, T, Hq) ||
+            rows_clash(a.qo, a.q, 1, T, Hq) || rows_meet(a.qo, Hq, a.k, Hkv, 1, T) || rows_meet(a.qo, Hq, a.v, Hkv, 1, T)))
     return S2O_ERR_INVALID_ARG;
+  const size_t cache = (size_t)cfg->num_pages * Hkv * cfg->page_size * kD * sizeof(uint16_t);
+  if (ranges_meet(k_cache, cache, v_cache, cache)) return S2O_ERR_INVALID_ARG;
   if ((int64_t)cfg->Hq + 2 * (int64_t)cfg->Hkv > 4096) return S2O_ERR_UNSUPPORTED_SHAPE;
   a.pos = positions;
   a.table = page_table; a.q_start = q_start; a.kv_len = kv_len;
@@ -340,9 +355,11 @@ s2o_status s2o_attention_paged(const s2o_cache_config* cfg, const uint16_t* Q, c
       (cfg->prefix_len > 0 && !prefix_pages))
     return S2O_ERR_INVALID_ARG;
   if (out_dtype != S2O_OUT_SAME && out_dtype != S2O_OUT_F32) return S2O_ERR_INVALID_ARG;
-  if (!aligned16(Q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(O) || O == Q ||
+  if (!aligned16(Q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(O) ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return S2O_ERR_INVALID_ARG;
+  const size_t rows = (size_t)cfg->Tq * cfg->Hq, row = kD * sizeof(uint16_t);
+  if (ranges_meet(O, rows * row * (out_dtype == S2O_OUT_F32 ? 2 : 1), Q, rows * row)) return S2O_ERR_INVALID_ARG;
   const int n = sm_count();
   const PagedPlan p = paged_plan(cfg, n);
   const PagedWs w = paged_layout(cfg, p, n, workspace);
@@ -360,11 +377,11 @@ s2o_status s2o_attention_paged(const s2o_cache_config* cfg, const uint16_t* Q, c
   a.beside = p.tiles;
   a.own_ns = p.R == 1 ? 520.f : 1100.f;
   CUtensorMap tmQ, tmK, tmV;
-  const uint64_t rows = (uint64_t)cfg->num_pages * cfg->Hkv * cfg->page_size;
+  const uint64_t cache_rows = (uint64_t)cfg->num_pages * cfg->Hkv * cfg->page_size;
   const uint32_t box = (uint32_t)std::min(cfg->page_size, 64);
   const bool fp16 = cfg->dtype == S2O_TYPE_FP16;
   if (p.chunks || p.tiles) {
-    if (!encode_rows_map(&tmK, k_cache, rows, box) || !encode_rows_map(&tmV, v_cache, rows, box)) return S2O_ERR_CUDA;
+    if (!encode_rows_map(&tmK, k_cache, cache_rows, box) || !encode_rows_map(&tmV, v_cache, cache_rows, box)) return S2O_ERR_CUDA;
     if (!encode_query_map(&tmQ, Q, cfg->Tq, cfg->Hq, g.G, kLq / g.G, fp16)) return S2O_ERR_CUDA;
     a.c = p.tile;
     a.other = p.decode;
@@ -375,7 +392,7 @@ s2o_status s2o_attention_paged(const s2o_cache_config* cfg, const uint16_t* Q, c
     ++t_launches;
   }
   if (!p.chunks) {
-    if (!encode_rows_map(&tmK, k_cache, rows, kPgSub) || !encode_rows_map(&tmV, v_cache, rows, kPgSub))
+    if (!encode_rows_map(&tmK, k_cache, cache_rows, kPgSub) || !encode_rows_map(&tmV, v_cache, cache_rows, kPgSub))
       return S2O_ERR_CUDA;
     a.c = p.decode;
     a.other = p.tile;

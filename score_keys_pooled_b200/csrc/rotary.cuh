@@ -26,6 +26,7 @@
 
 #include <cuda_fp16.h>
 
+#include "row_views.h"
 #include "s2o_common.cuh"
 
 namespace s2o {
@@ -39,11 +40,6 @@ struct RotaryTable {
   uint8_t axis[64];
   int rot, adjacent, naxes;
   float sign;         // -1: inverse
-};
-
-struct RowView {
-  uint16_t* p;
-  int64_t sb, st, sh;  // strides in elements
 };
 
 template <bool FP16>

@@ -111,6 +111,30 @@ def test_rotary_in_place_into_views_and_between():
     assert bool(((back - x).double().abs() <= 2 * half_step(torch.float16) * 1.5 * mag.double() + 1e-6).all())
 
 
+def test_rotary_in_one_buffer():
+    """Queries and keys side by side in one buffer, in place and from one into
+    another, token-major and head-major: views that lie within one another's reach
+    and share no row."""
+    r = s2o.make_rotary(128)
+    B, N, Hq, Hkv = 2, 19, 6, 2
+    pos = torch.arange(B * N, device="cuda", dtype=torch.int32).view(1, B, N)
+    packed = torch.randn(B, N, Hq + 2 * Hkv, 128, device="cuda").bfloat16()
+    q, k, v = packed[:, :, :Hq], packed[:, :, Hq:Hq + Hkv], packed[:, :, Hq + Hkv:].clone()
+    wq, wk = (x.clone() for x in s2o.rotary(r, q, k, pos))
+    heads = torch.empty(B, Hq + Hkv, N, 128, device="cuda", dtype=torch.bfloat16)
+    hq, hk = heads[:, :Hq].transpose(1, 2), heads[:, Hq:].transpose(1, 2)
+    s2o.rotary(r, q, k, pos, q_out=hq, k_out=hk)
+    assert torch.equal(hq, wq) and torch.equal(hk, wk)
+    s2o.rotary(r, q, k, pos, q_out=q, k_out=k)
+    assert torch.equal(q, wq) and torch.equal(k, wk) and torch.equal(packed[:, :, Hq + Hkv:], v)
+    s2o.rotary(r, hq[:, :, 3:], hq[:, :, :3], pos, q_out=hq[:, :, 3:], k_out=hq[:, :, :3], inverse=True)
+    assert s2o.last_device_error() == 0
+    for bad in (dict(q_out=hq[:, :, :3], k_out=hq[:, :, 2:4]), dict(q_out=hq[:, :, 1:4], k_out=hk)):
+        with pytest.raises(s2o.S2OError) as e:
+            s2o.rotary(r, hq[:, :, :3], hk, pos, **bad)
+        assert e.value.code == 1 and s2o.last_launch_count() == 0
+
+
 # --- append -------------------------------------------------------------------------------------------
 
 

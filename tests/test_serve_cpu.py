@@ -1,6 +1,7 @@
 """The serving calls without a GPU: the oracle's own pins, every refusal that
 is made before a launch, and the host-side arithmetic of the configs."""
 import ctypes
+import subprocess
 
 import numpy as np
 import pytest
@@ -228,3 +229,113 @@ def test_binding_refuses_tensors_the_call_was_not_made_for():
 def test_status_of_a_bad_cache(L):
     assert s2o.status_string(8) == "page, length or token range out of range"
     assert s2o.STATUS[8] == "S2O_ERR_BAD_CACHE"
+
+
+VIEWS = r"""
+#include "row_views.h"
+using namespace s2o;
+extern "C" {
+int meet_self(int64_t p, const int64_t* s, const int64_t* n) {
+  return rows_meet(RowView{reinterpret_cast<uint16_t*>(p), s[0], s[1], s[2]}, n[0], n[1], n[2]);
+}
+int meet_two(int64_t p, const int64_t* s, int64_t Hx, int64_t q, const int64_t* u, int64_t Hy, const int64_t* n) {
+  return rows_meet(RowView{reinterpret_cast<uint16_t*>(p), s[0], s[1], s[2]}, Hx,
+                   RowView{reinterpret_cast<uint16_t*>(q), u[0], u[1], u[2]}, Hy, n[0], n[1]);
+}
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def views(tmp_path_factory):
+    d = tmp_path_factory.mktemp("views")
+    (d / "v.cpp").write_text(VIEWS)
+    subprocess.run(["g++", "-std=c++17", "-O2", "-shared", "-fPIC", "-I", build.CSRC, "-o", str(d / "v.so"),
+                    str(d / "v.cpp")], check=True)
+    lib = ctypes.CDLL(str(d / "v.so"))
+    arr = lambda x: (ctypes.c_int64 * 3)(*x)
+    i64 = ctypes.c_int64
+    return (lambda p, s, n: bool(lib.meet_self(i64(p), arr(s), arr(n))),
+            lambda p, s, Hx, q, u, Hy, B, N: bool(lib.meet_two(i64(p), arr(s), i64(Hx), i64(q), arr(u), i64(Hy), arr((B, N, 0)))))
+
+
+def elements(p, s, n):
+    """Element ranges' first numbers of every row, from a byte address."""
+    at = p // 2 + sum(np.arange(k).reshape([-1 if i == j else 1 for j in range(3)]) * st
+                      for i, (k, st) in enumerate(zip(n, s)))
+    return at.reshape(-1)
+
+
+def some_strides(rng, n):
+    """Nested in a random order, packed with room, or anything."""
+    kind = rng.integers(3)
+    if kind == 2:
+        return [int(x) * 8 for x in rng.integers(-40, 200, 3)]
+    s, reach = [0, 0, 0], 128 + 8 * int(rng.integers(0, 20)) * int(kind)
+    for i in rng.permutation(3):
+        s[i] = reach
+        reach = reach * n[i] + 8 * int(rng.integers(0, 30)) * int(kind)
+    return s
+
+
+def test_rows_that_fall_on_one_another_are_seen(views):
+    """Against a count of every element, on random views: of one view, and of two
+    with the same strides (exact); of two with other strides no meeting is claimed
+    that is none."""
+    meet_self, meet_two = views
+    rng = np.random.default_rng(7)
+    base, hits = 1 << 30, [0, 0, 0, 0]
+    for _ in range(6000):
+        B, N, Hx, Hy = (int(x) for x in rng.integers(1, [4, 7, 6, 6]))
+        s = some_strides(rng, (B, N, max(Hx, Hy) + 2))
+        x = np.sort(elements(base, s, (B, N, Hx)))
+        want = bool((np.diff(x) < 128).any())
+        assert meet_self(base, s, (B, N, Hx)) == want, (s, B, N, Hx)
+        hits[want] += 1
+        q = base + 16 * int(rng.integers(-60, 200)) if rng.random() < .5 else base + 2 * s[2] * int(rng.integers(-2, 8))
+        u = s if rng.random() < .7 else some_strides(rng, (B, N, Hy))
+        y = elements(q, u, (B, N, Hy))
+        want = bool((np.abs(x[:, None] - y[None]) < 128).any())
+        got = meet_two(base, s, Hx, q, u, Hy, B, N)
+        assert got == want if u is s else want or not got, (s, u, B, N, Hx, Hy, q - base)
+        hits[2 + want] += 1
+    assert min(hits) > 500, hits
+
+
+def test_whole_buffers_in_another_order_are_seen(views):
+    """Head-major rows over token-major ones, a window of them, strides that no memory has."""
+    _, meet_two = views
+    B, N, H = 2, 9, 5
+    head, token = (H * N * 128, 128, N * 128), (N * H * 128, H * 128, 128)
+    packed = (N * 9 * 128, 9 * 128, 128)
+    assert meet_two(1 << 20, head, H, 1 << 20, token, H, B, N)
+    assert meet_two(1 << 20, head, H, (1 << 20) + 2 * 128 * 7, token, H, B, N)
+    assert not meet_two(1 << 20, head, H, (1 << 20) + 2 * 128 * B * N * H, token, H, B, N)
+    assert meet_two(1 << 20, packed, 5, 1 << 20, head, H, B, N)
+    assert not meet_two(1 << 20, packed, 5, (1 << 20) + 5 * 256, packed, 4, B, N)
+    assert meet_two(1 << 20, packed, 5, (1 << 20) + 4 * 256, packed, 4, B, N)
+    far = ((1 << 63) - 8, (1 << 62), -(1 << 63))
+    assert meet_two(1 << 20, far, 5, 1 << 20, far, 5, B, N)
+
+
+def test_outputs_in_the_way_are_refused(L):
+    """An output on itself, on another output, or on an input it is not the place of."""
+    r, M, X = s2o.make_rotary(128), 1 << 20, 1 << 30
+    base = lambda **kw: {**dict(q=view(M), k=view(2 * M), qo=view(X), ko=view(X + M)), **kw}
+    call = lambda a: L.s2o_rotary(r, 0, 1, 4, 2, 1, a["q"], a["k"], GOOD, a["qo"], a["ko"], 0, None)
+    for bad in (dict(qo=view(X, t=64)), dict(qo=view(X, t=128, h=256)), dict(ko=view(X + 256)), dict(ko=view(X)),
+                dict(qo=view(M, t=256)), dict(qo=view(M + 2 * 1024)), dict(ko=view(M + 256)), dict(qo=view(2 * M))):
+        assert call(base(**bad)) == 1, list(bad)
+    c = cache()
+    good = dict(q=view(M), k=view(2 * M), v=view(3 * M), kc=ctypes.c_void_p(X), vc=ctypes.c_void_p(X + M), qo=view(M))
+    for bad in (dict(qo=view(2 * M)), dict(qo=view(3 * M + 256)), dict(qo=view(M + 256)), dict(qo=view(M, t=128, h=384)),
+                dict(qo=view(X, t=512, h=64)), dict(vc=ctypes.c_void_p(X + 256))):
+        a = {**good, **bad}
+        assert L.s2o_cache_append(c, r, a["q"], a["k"], a["v"], None, GOOD, GOOD, GOOD, a["kc"], a["vc"], a["qo"],
+                                  None) == 1, list(bad)
+    need = s2o.attention_paged_workspace_size(c)
+    p = ctypes.c_void_p
+    for O, f32 in ((X + 16, 0), (X + 3 * 8 * 256 - 16, 0), (X - 3 * 8 * 512 + 16, 1)):  # Q is 3 x 8 rows
+        assert L.s2o_attention_paged(c, p(X), GOOD, GOOD, GOOD, GOOD, GOOD, GOOD, p(O), f32, None, p(1 << 40), need,
+                                     None) == 1
+    assert s2o.last_launch_count() == 0
