@@ -389,7 +389,8 @@ typedef struct s2o_rotary_config {
 } s2o_rotary_config;
 
 /* Rows of 128 contiguous elements at ptr + b stride_b + t stride_t + h
- * stride_h (strides in elements, multiples of 8; ptr 16-byte aligned). */
+ * stride_h (strides in elements, multiples of 8 where there is more than one
+ * b, t or h, else unused; ptr 16-byte aligned). */
 typedef struct s2o_view {
   void* ptr;
   int64_t stride_b, stride_t, stride_h;

@@ -24,14 +24,15 @@ s2o_status rotary_table(const s2o_rotary_config* r, bool inverse, RotaryTable* t
   return S2O_OK;
 }
 
-bool take_view(const s2o_view* v, RowView* out) {
+// A view of B x N x H rows.  Rows stay 16-byte aligned; a stride that no row is
+// reached by says nothing.
+bool take_view(const s2o_view* v, int64_t B, int64_t N, int64_t H, RowView* out) {
   if (!v->ptr || !aligned16(v->ptr)) return false;
-  if (v->stride_b % 8 || v->stride_t % 8 || v->stride_h % 8) return false;  // rows stay 16-byte aligned
   out->p = static_cast<uint16_t*>(v->ptr);
-  out->sb = v->stride_b;
-  out->st = v->stride_t;
-  out->sh = v->stride_h;
-  return true;
+  out->sb = B > 1 ? v->stride_b : 0;
+  out->st = N > 1 ? v->stride_t : 0;
+  out->sh = H > 1 ? v->stride_h : 0;
+  return out->sb % 8 == 0 && out->st % 8 == 0 && out->sh % 8 == 0;
 }
 
 // an output where the input it is made from has other rows: in place means in
@@ -274,8 +275,8 @@ s2o_status s2o_rotary(const s2o_rotary_config* rotary, int32_t dtype, int32_t B,
   if ((int64_t)Hq + Hkv > 4096) return S2O_ERR_UNSUPPORTED_SHAPE;
   if (!positions || (Hq && (!q || !q_out)) || (Hkv && (!k || !k_out))) return S2O_ERR_INVALID_ARG;
   std::memset(&a.q, 0, 4 * sizeof(RowView));
-  if (Hq && (!take_view(q, &a.q) || !take_view(q_out, &a.qo))) return S2O_ERR_INVALID_ARG;
-  if (Hkv && (!take_view(k, &a.k) || !take_view(k_out, &a.ko))) return S2O_ERR_INVALID_ARG;
+  if (Hq && (!take_view(q, B, N, Hq, &a.q) || !take_view(q_out, B, N, Hq, &a.qo))) return S2O_ERR_INVALID_ARG;
+  if (Hkv && (!take_view(k, B, N, Hkv, &a.k) || !take_view(k_out, B, N, Hkv, &a.ko))) return S2O_ERR_INVALID_ARG;
   // rows are turned in any order: none may be written twice, or before another is made from it
   if ((Hq && (rows_meet(a.qo, B, N, Hq) || rows_clash(a.qo, a.q, B, N, Hq))) ||
       (Hkv && (rows_meet(a.ko, B, N, Hkv) || rows_clash(a.ko, a.k, B, N, Hkv))) ||
@@ -311,9 +312,9 @@ s2o_status s2o_cache_append(const s2o_cache_config* cfg, const s2o_rotary_config
     return S2O_ERR_INVALID_ARG;
   if (!aligned16(k_cache) || !aligned16(v_cache)) return S2O_ERR_INVALID_ARG;
   std::memset(&a.q, 0, 4 * sizeof(RowView));
-  if (!take_view(k, &a.k) || !take_view(v, &a.v)) return S2O_ERR_INVALID_ARG;
   const int T = cfg->Tq, Hq = cfg->Hq, Hkv = cfg->Hkv;
-  if (q && (!take_view(q, &a.q) || !take_view(q_out, &a.qo) || rows_meet(a.qo, 1, T, Hq) ||
+  if (!take_view(k, 1, T, Hkv, &a.k) || !take_view(v, 1, T, Hkv, &a.v)) return S2O_ERR_INVALID_ARG;
+  if (q && (!take_view(q, 1, T, Hq, &a.q) || !take_view(q_out, 1, T, Hq, &a.qo) || rows_meet(a.qo, 1, T, Hq) ||
             rows_clash(a.qo, a.q, 1, T, Hq) || rows_meet(a.qo, Hq, a.k, Hkv, 1, T) || rows_meet(a.qo, Hq, a.v, Hkv, 1, T)))
     return S2O_ERR_INVALID_ARG;
   const size_t cache = (size_t)cfg->num_pages * Hkv * cfg->page_size * kD * sizeof(uint16_t);

@@ -135,6 +135,29 @@ def test_rotary_in_one_buffer():
         assert e.value.code == 1 and s2o.last_launch_count() == 0
 
 
+def test_dimensions_of_one_may_have_any_stride():
+    """One batch, one token, one head: torch leaves odd strides there."""
+    r = s2o.make_rotary(128)
+    pos = torch.full((1, 1, 1), 77, device="cuda", dtype=torch.int32)
+    x = torch.randn(1, 1, 1, 128, device="cuda").bfloat16()
+    want, _ = s2o.rotary(r, x, None, pos)
+    odd = x.as_strided((1, 1, 1, 128), (1, 3, 5, 1))
+    out = torch.empty_like(x).as_strided((1, 1, 1, 128), (7, 1, 1, 1))
+    s2o.rotary(r, odd, None, pos, q_out=out)
+    assert torch.equal(out, want)
+    y = torch.randn(5, 128, 1, device="cuda").bfloat16().transpose(1, 2)  # [5, 1, 128], head stride 1
+    assert y.stride(1) == 1
+    pos = torch.arange(5, device="cuda", dtype=torch.int32).view(1, 1, 5)
+    want, _ = s2o.rotary(r, y.contiguous()[None], None, pos)
+    got, _ = s2o.rotary(r, y[None], None, pos)
+    assert torch.equal(got, want)
+    b = Batch([5], [9], Hq=1, Hkv=1)
+    kc, vc = b.k.cuda(), b.v.cuda()
+    s2o.cache_append(b.cfg, None, y, y, kc, vc, b.table.cuda(), b.q_start.cuda(), b.kv_len.cuda())
+    assert s2o.last_device_error() == 0
+    assert torch.equal(kc[b.table[0, 0].long(), 0, 4:9], y[:, 0]) and torch.equal(vc[b.table[0, 0].long(), 0, 4:9], y[:, 0])
+
+
 # --- append -------------------------------------------------------------------------------------------
 
 

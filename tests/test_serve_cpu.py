@@ -174,6 +174,18 @@ def test_append_refusals(L):
     assert s2o.last_launch_count() == 0
 
 
+def test_a_stride_that_reaches_no_row_says_nothing(L):
+    """Of views with one token only the head stride counts, and stride_b of the append's
+    never: such calls come past the views (to the refusal of too many heads)."""
+    r, M = s2o.make_rotary(128), 1 << 30
+    for T, odd in ((1, dict(b=3, t=1)), (1, dict(b=-1)), (2, dict(b=7)), (2, dict(b=1, t=1)), (1, dict(h=4))):
+        c = cache(Hq=4096, Hkv=64, Tq=T)
+        a = [view(i * M, **{**dict(t=1 << 20), **odd}) for i in range(1, 5)]
+        got = L.s2o_cache_append(c, r, a[0], a[1], a[2], None, GOOD, GOOD, GOOD, ctypes.c_void_p(5 * M),
+                                 ctypes.c_void_p(6 * M), a[3], None)
+        assert got == (2 if "h" not in odd and odd.get("t", 8) % 8 * (T - 1) == 0 else 1), (T, odd)
+
+
 def test_rotary_refusals(L):
     r = s2o.make_rotary(128)
     good = [r, 0, 1, 4, 2, 1, view(), view(), GOOD, view(), view(), 0, None]
