@@ -529,6 +529,8 @@ def attention_paged(cfg: CacheConfig, q, k_cache, v_cache, page_table, q_start, 
     if lse is None:
         lse = _empty((T, cfg.Hq), torch.float32, dev, stream)
     if workspace is None:
+        if dev.type != "cuda":
+            _refuse(f"attention_paged: the tensors are on {dev}, not on a CUDA device")
         with torch.cuda.device(dev):
             workspace = _empty((attention_paged_workspace_size(cfg),), torch.uint8, dev, stream)
     elif workspace.device != dev or not workspace.is_contiguous():

@@ -238,6 +238,15 @@ def test_binding_refuses_tensors_the_call_was_not_made_for():
         assert e.value.code == 1
 
 
+def test_attention_without_a_workspace_refuses_host_tensors():
+    c = cache()
+    kc, vc = s2o.alloc_cache(c, "cpu")
+    table, qs, kl, pre = (torch.zeros(s, dtype=torch.int32) for s in ((2, 4), (3,), (2,), (2,)))
+    with pytest.raises(s2o.S2OError) as e:
+        s2o.attention_paged(c, torch.zeros(3, 8, 128, dtype=torch.bfloat16), kc, vc, table, qs, kl, prefix_pages=pre)
+    assert e.value.code == 1
+
+
 def test_status_of_a_bad_cache(L):
     assert s2o.status_string(8) == "page, length or token range out of range"
     assert s2o.STATUS[8] == "S2O_ERR_BAD_CACHE"
