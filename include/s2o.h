@@ -367,7 +367,9 @@ s2o_status s2o_prefill_host(const s2o_config* cfg, const uint16_t* Q_host, const
  * Element types: bf16 or fp16 (S2O_TYPE_*), head dimension 128.
  */
 enum { S2O_TYPE_BF16 = 0, S2O_TYPE_FP16 = 1 };
-enum { S2O_OUT_SAME = 0 }; /* s2o_attention_paged: O in the cache's type (or S2O_OUT_F32) */
+/* s2o_attention_paged: O in the cache's type, or S2O_OUT_F32: the sums unrounded,
+ * of probabilities that are rounded to the cache's type all the same */
+enum { S2O_OUT_SAME = 0 };
 
 /*
  * Rotation of a head row x at the positions p[0 .. naxes) of its token:
@@ -468,18 +470,25 @@ s2o_status s2o_cache_append(const s2o_cache_config* cfg, const s2o_rotary_config
 /*
  * s2o_attention_paged -- exact softmax attention of the new tokens over the
  * cache: token i of a sequence's own keys sees the whole prefix and the own
- * keys 0 .. i.  The prefix is read once for the whole batch, each own key once.
+ * keys 0 .. i.  How often the cache is read goes by the call's sizes: the prefix
+ * once for every 16, 32 or 256 rows of the batch or, where that costs less, once
+ * for every row tile of a sequence (from L2 as far as it fits); own keys once for
+ * each row tile of their sequence, of which single tokens and drafts have one.
  *   Q    device [Tq, Hq, 128], contiguous
  *   O    out, device [Tq, Hq, 128], in the cache's type (S2O_OUT_SAME) or
  *        fp32; apart from Q's memory
  *   lse  out, device fp32 [Tq, Hq]: log sum_j exp(s_ij); or NULL
  *   workspace  device scratch of s2o_attention_paged_workspace_size() bytes
  *        (on the device the call runs on), 256-byte aligned; contents need no
- *        initialisation; calls whose work may overlap need one each
+ *        initialisation; calls whose work may overlap need one each.  The size
+ *        follows the way a call is put together, not its rows alone: a step of
+ *        single tokens may need more than a chunk (1 and 64 tokens behind 32768
+ *        keys, 32 heads on 8: 59 and 42 MB).  Ask for every config that shares
+ *        one and take the largest
  * Sums and accumulators are fp32; probabilities are rounded to the cache's
- * type for the product with V.  Cached rows below the lengths must be finite;
- * what pages hold behind them does not matter.  The result depends on the
- * inputs and the device's SM count alone (no atomics).
+ * type for the product with V, with S2O_OUT_F32 too.  Cached rows below the
+ * lengths must be finite; what pages hold behind them does not matter.  The
+ * result depends on the inputs and the device's SM count alone (no atomics).
  */
 s2o_status s2o_attention_paged_workspace_size(const s2o_cache_config* cfg, size_t* bytes);
 s2o_status s2o_attention_paged(const s2o_cache_config* cfg, const uint16_t* Q, const uint16_t* k_cache,

@@ -502,7 +502,8 @@ def attention_paged_workspace_size(cfg: CacheConfig) -> int:
 
 def alloc_attention_paged(cfg: CacheConfig, device="cuda"):
     """A workspace for attention_paged calls of this config on `device` (one per
-    stream or captured graph whose work may overlap another's)."""
+    stream or captured graph whose work may overlap another's).  Smaller batches may
+    need more (see include/s2o.h): calls of several configs share the largest one."""
     import torch
     with torch.cuda.device(device):
         return torch.empty(attention_paged_workspace_size(cfg), dtype=torch.uint8, device=device)
@@ -512,7 +513,8 @@ def attention_paged(cfg: CacheConfig, q, k_cache, v_cache, page_table, q_start, 
                     lse=None, workspace=None, out_dtype: int = OUT_SAME, stream=None):
     """s2o_attention_paged: q [Tq, Hq, 128] over the caches; returns (O, lse).
     O, lse (float32 [Tq, Hq]) and the workspace are allocated when not given;
-    rows behind q_start[nseq] are left as they were."""
+    rows behind q_start[nseq] are left as they were.  OUT_F32 leaves out O's own
+    rounding; the probabilities are of the cache's type in either form."""
     import torch
     dev, t, T = q.device, _torch_type(cfg.dtype), cfg.Tq
     qp = _plain(q, "attention_paged: q", (T, cfg.Hq, 128), t, dev)

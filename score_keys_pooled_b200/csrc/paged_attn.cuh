@@ -18,7 +18,7 @@
 //     to 0.9 us of latency (two chains of products with the softmax between)
 //     and a piece 2.2 us (sequence numbers, first loads, results), while the
 //     other streams' reads go on: 16 sequences of up to 32K keys, 1.07 GB, take
-//     180 us, 6.0 TB/s, 91 % of the measured copy rate; even shares on SMs that
+//     187 us, 5.8 TB/s, 88 % of the measured copy rate; even shares on SMs that
 //     are not equally near the memory (warps end between 119 and 174 us) are
 //     what is left.  One ring for the whole CTA, its 64-key stages cut into
 //     slices over four or eight warps and joined in shared memory at the end of

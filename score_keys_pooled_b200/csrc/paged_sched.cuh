@@ -81,7 +81,8 @@ __host__ __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
   return quot_long(a, b);
 }
 
-// sum over i < n of floor((a i + b) / m), n, a, b >= 0, m > 0
+// sum over i < n of floor((a i + b) / m), n, a, b >= 0, m > 0: the well-known
+// recursion of Euclid's algorithm (whole parts out, then the axes swapped)
 static __host__ __device__ __noinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
   int64_t r = 0;
   while (n > 0) {

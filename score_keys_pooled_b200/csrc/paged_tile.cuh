@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kAttn2Threads, 1)
     const int bi = lane >> 1, half = lane & 1;  // this lane's box of a tile
     bool ok = true;
     uint32_t it = 0, vt = 0;
-// own chunks are read by tile after tile, and the prefix by all of them
+    // own chunks are read by tile after tile, and the prefix by all of them
     const uint64_t policy = keys_policy(!a.c.own_items && (sc.npt <= 1 || sc.team > 1));
     SplitItem split = {0, 0, 0, 0};
     for (int pi = 0; ok; ++pi) {

@@ -18,9 +18,9 @@
 // written once, 16 bytes a load, eight lanes a row (a lane owns eight pairs:
 // two 16-byte chunks).  A block takes the rows of `tb` tokens; each token's
 // angles are formed once per block and shared by all of its heads.  The
-// rotation of 131072 tokens of 40 heads, 2.68 GB, takes 430 us, 6.2 TB/s or 95 %
+// rotation of 131072 tokens of 40 heads, 2.68 GB, takes 442 us, 6.1 TB/s or 93 %
 // of the measured copy rate; the append of 14336 tokens, 353 MB whose cache rows
-// lie 256 bytes here and there, 70 us, 5.0 TB/s; one row more or fewer in flight
+// lie 256 bytes here and there, 70 us, 5.1 TB/s; one row more or fewer in flight
 // a thread and larger or smaller blocks made either slower or no faster.
 #pragma once
 

@@ -1,6 +1,6 @@
 // C ABI of the S2O library: argument checks, workspace layout and launches.
-// Everything that computes runs in the kernels of pool_score.cuh,
-// seg_sort.cuh and sparse_attn.cuh.
+// Everything that computes runs in the kernels of the .cuh files; the serving
+// calls' entries are in paged_api.cuh.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
